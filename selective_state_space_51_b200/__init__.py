@@ -22,6 +22,17 @@ importing works but the first call raises: there is no fallback path.
                      save_checkpoints=True)
     grads = scan.backward(x, delta, A_log, B, C, dy, D=D, z=z,
                           delta_bias=bias, reuse_checkpoints=True)
+
+Beside the scan, with one decay a head instead of one a channel and state
+(include/ssm_linattn.h), and the norm around either (include/ssm_layernorm.h):
+
+    attn, norm = LinearAttention(device=0), LayerNorm(device=0)
+    y, h_last = attn(q, k, v, log_decay=g, h0=state)
+    y_t = attn.step(q_t, k_t, v_t, state, log_decay=g_t)
+    grads = attn.backward(q, k, v, dy, log_decay=g)
+    out = norm(x, weight=w, bias=b, residual=r)   # y, sum, mean, rstd
+    grads = norm.backward(dy, out["sum"], out["mean"], out["rstd"], weight=w,
+                          bias=b)
 """
 from __future__ import annotations
 
@@ -57,6 +68,12 @@ SSM_VARIANT_CHUNKED = 2
 class ssm_scan_dims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
                 ("dim", ctypes.c_int64), ("dstate", ctypes.c_int64)]
+
+
+class ssm_linattn_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "batch", "seqlen", "heads", "groups", "dk", "dv", "q_stride",
+        "k_stride", "v_stride")]
 
 
 class SsmScanError(RuntimeError):
@@ -112,6 +129,33 @@ def library() -> ctypes.CDLL:
                 i32, vp, vp, vp, vp, vp, vp, vp, vp, u32, vp, vp, vp,
                 ssm_scan_dims, i32, i32, vp, vp]
             lib.ssm_scan_fwd_static_scratch.restype = i32
+            dims = ssm_linattn_dims
+            lib.ssm_linattn_workspace.argtypes = [
+                i32, dims, i32, i32, ctypes.POINTER(ctypes.c_size_t)]
+            lib.ssm_linattn_workspace.restype = i32
+            lib.ssm_linattn_fwd.argtypes = [
+                i32, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp,
+                ctypes.c_size_t, dims, i32, vp]
+            lib.ssm_linattn_fwd.restype = i32
+            lib.ssm_linattn_step.argtypes = [
+                i32, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, dims, i32,
+                vp]
+            lib.ssm_linattn_step.restype = i32
+            lib.ssm_linattn_bwd.argtypes = [
+                i32, vp, vp, vp, vp, vp, ctypes.c_float] + [vp] * 11 + [
+                ctypes.c_size_t, dims, i32, vp]
+            lib.ssm_linattn_bwd.restype = i32
+            i64 = ctypes.c_int64
+            lib.ssm_layernorm_workspace.argtypes = [
+                i32, i64, i64, i32, ctypes.POINTER(ctypes.c_size_t)]
+            lib.ssm_layernorm_workspace.restype = i32
+            lib.ssm_layernorm_fwd.argtypes = [
+                i32, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, i64, i64,
+                i32, vp]
+            lib.ssm_layernorm_fwd.restype = i32
+            lib.ssm_layernorm_bwd.argtypes = [i32] + [vp] * 10 + [
+                ctypes.c_size_t, i64, i64, i32, vp]
+            lib.ssm_layernorm_bwd.restype = i32
             lib.ssm_measure_ex2_rate.argtypes = [i32,
                                                  ctypes.POINTER(ctypes.c_double)]
             lib.ssm_measure_ex2_rate.restype = i32
@@ -418,3 +462,10 @@ class SelectiveScan:
                          delta_bias, flags, h0, y, h_last, (b, L, E, N),
                          dtype, stream)
         return (y, h_last) if return_last_state else y
+
+
+from .layernorm import (LayerNorm, ssm_layernorm_bwd,  # noqa: E402,F401
+                        ssm_layernorm_fwd, ssm_layernorm_workspace)
+from .linattn import (LinearAttention, ssm_linattn_bwd,  # noqa: E402,F401
+                      ssm_linattn_fwd, ssm_linattn_step,
+                      ssm_linattn_workspace)

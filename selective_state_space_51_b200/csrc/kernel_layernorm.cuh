@@ -1,0 +1,375 @@
+// Layer norm over the last dimension, with the residual sum in front, and its
+// backward pass. Both are bound by DRAM: the row is read once into registers,
+// and everything else happens there.
+//
+//   s = x (+ residual, rounded to the stream's type: the sum is stored and
+//       the norm reads what is stored, so that the backward pass, which reads
+//       the stored sum again, differentiates exactly this)
+//   mean = sum(s) / D, var = sum((s - mean)^2) / D (two passes over registers:
+//       no cancellation however far the mean is from zero)
+//   y = (s - mean) rstd w + b,  rstd = 1 / sqrt(var + eps)
+//
+// Backward, with xhat = (s - mean) rstd and u = dy w:
+//   dx = rstd (u - mean(u) - xhat mean(u xhat)) + dsum
+//   dw = sum over rows of dy xhat,  db = sum over rows of dy
+// dw and db: a thread keeps its columns over all rows its block takes, blocks
+// write one partial row each, and a second kernel adds those in a fixed order.
+// No atomics: every result is the same on every run.
+//
+// Layout. A row belongs to G lanes of a warp (G < 32, short rows) or to
+// `wpr` whole warps; a thread holds N groups of V consecutive elements (V: 16
+// bytes where rows allow it, else 1), group i at column (i * lanes + lane) V.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+namespace ssm {
+
+struct NormParams {
+  const void *x, *residual;      // [rows, dim]
+  const float *weight, *bias;    // [dim] or nullptr
+  void *y, *sum;                 // [rows, dim]; sum or nullptr
+  float *mean, *rstd;            // [rows] (forward: or nullptr)
+  float eps;
+  int64_t rows;
+  int dim;
+  int wpr;                       // warps per row (G == 32)
+  // backward
+  const void *dy, *dsum;         // [rows, dim]; dsum or nullptr
+  void *dx;
+  float *part;                   // [2, parts, dim]: dw's, db's, or nullptr
+  float *dweight, *dbias;
+  int parts;                     // partial rows: blocks of the first kernel
+};
+
+namespace norm {
+
+using bf16 = __nv_bfloat16;
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
+
+// V elements from (streamed: read once) or to global memory.
+template <typename T, int V>
+__device__ __forceinline__ void load(const T *p, float (&f)[V]) {
+  if constexpr (V == 1) {
+    f[0] = to_f(*p);
+  } else if constexpr (sizeof(T) == 4) {
+    const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
+    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+  } else {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = __uint_as_float(w[j] << 16);
+      f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store(T *p, const float (&f)[V]) {
+  if constexpr (V == 1) {
+    *p = T(f[0]);
+  } else if constexpr (sizeof(T) == 4) {
+    __stcs(reinterpret_cast<float4 *>(p),
+           make_float4(f[0], f[1], f[2], f[3]));
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+          : "=r"(w[j])
+          : "f"(f[2 * j + 1]), "f"(f[2 * j]));
+    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
+  }
+}
+
+// V parameters (kept in cache: every row reads them).
+template <int V>
+__device__ __forceinline__ void load_param(const float *p, float (&f)[V]) {
+  if constexpr (V == 1) {
+    f[0] = __ldg(p);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4 *>(p + j));
+      f[j] = v.x; f[j + 1] = v.y; f[j + 2] = v.z; f[j + 3] = v.w;
+    }
+  }
+}
+
+// Sums over a row's threads. `red` has room for two values of each warp, for
+// two calls in turn (`slot` 0, 1), so that one barrier a call is enough.
+template <int G>
+__device__ __forceinline__ void row_sum2(float &a, float &b, int wpr,
+                                         float2 *red, int slot) {
+#pragma unroll
+  for (int d = G / 2; d > 0; d >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, d);
+    b += __shfl_xor_sync(0xffffffffu, b, d);
+  }
+  if constexpr (G == 32) {
+    if (wpr > 1) {
+      const int warp = threadIdx.x / 32;
+      float2 *r = red + slot * 32;
+      if (threadIdx.x % 32 == 0) r[warp] = make_float2(a, b);
+      __syncthreads();
+      const int first = warp / wpr * wpr;
+      a = b = 0.0f;
+      for (int w = 0; w < wpr; ++w) {
+        const float2 v = r[first + w];
+        a += v.x;
+        b += v.y;
+      }
+    }
+  }
+}
+
+template <typename T, int V, int N, int G>
+__global__ void __launch_bounds__(512)
+    layernorm_fwd_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float2 red[64];
+  const int lanes = G < 32 ? G : 32 * p.wpr;       // threads of a row
+  const int per = blockDim.x / lanes;              // rows of a block
+  const int lane = threadIdx.x % lanes;
+  const float inv = 1.0f / float(p.dim);
+  const int64_t steps = (p.rows + per - 1) / per;
+  for (int64_t st = blockIdx.x; st < steps; st += gridDim.x) {
+    const int64_t row = st * per + threadIdx.x / lanes;
+    const bool in = row < p.rows;
+    const int64_t base = row * p.dim;
+    float f[N][V];
+    float s = 0.0f, none = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * lanes + lane) * V;
+#pragma unroll
+      for (int j = 0; j < V; ++j) f[i][j] = 0.0f;
+      if (in && c < p.dim)
+        load<T, V>(static_cast<const T *>(p.x) + base + c, f[i]);
+    }
+    if (p.residual) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = (i * lanes + lane) * V;
+        if (in && c < p.dim) {
+          float r[V];
+          load<T, V>(static_cast<const T *>(p.residual) + base + c, r);
+#pragma unroll
+          for (int j = 0; j < V; ++j) f[i][j] = to_f(T(f[i][j] + r[j]));
+          if (p.sum) store<T, V>(static_cast<T *>(p.sum) + base + c, f[i]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) s += f[i][j];
+    row_sum2<G>(s, none, p.wpr, red, 0);
+    const float mean = s * inv;
+    float q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * lanes + lane) * V;
+      if (c < p.dim) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float d = f[i][j] - mean;
+          q = fmaf(d, d, q);
+        }
+      }
+    }
+    row_sum2<G>(q, none, p.wpr, red, 1);
+    const float rstd = 1.0f / sqrtf(fmaf(q, inv, p.eps));
+    if (in && lane == 0) {
+      if (p.mean) p.mean[row] = mean;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * lanes + lane) * V;
+      if (in && c < p.dim) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[i][j] = (f[i][j] - mean) * rstd;
+        if (p.weight) {
+          float w[V];
+          load_param<V>(p.weight + c, w);
+#pragma unroll
+          for (int j = 0; j < V; ++j) f[i][j] *= w[j];
+        }
+        if (p.bias) {
+          float w[V];
+          load_param<V>(p.bias + c, w);
+#pragma unroll
+          for (int j = 0; j < V; ++j) f[i][j] += w[j];
+        }
+        store<T, V>(static_cast<T *>(p.y) + base + c, f[i]);
+      }
+    }
+  }
+}
+
+// Columns sums of short rows go over many rows a thread: every kFold rows the
+// running sums are folded into a second pair, so that the rounding of a long
+// sum does not grow with its length.
+constexpr int kFold = 32;
+
+template <typename T, int V, int N, int G>
+__global__ void __launch_bounds__(512)
+    layernorm_bwd_kernel(const __grid_constant__ NormParams p) {
+  constexpr bool FOLD = N * V <= 8;
+  __shared__ float2 red[64];
+  extern __shared__ float cols[];  // [per - 1, 2, dim] at the end
+  const int lanes = G < 32 ? G : 32 * p.wpr;
+  const int per = blockDim.x / lanes;
+  const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes;
+  const float inv = 1.0f / float(p.dim);
+  const int64_t steps = (p.rows + per - 1) / per;
+  float dw[N][V], db[N][V], dw2[N][V], db2[N][V];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      dw[i][j] = db[i][j] = dw2[i][j] = db2[i][j] = 0.0f;
+  int fold = 0, slot = 0;
+  for (int64_t st = blockIdx.x; st < steps; st += gridDim.x, slot ^= 1) {
+    const int64_t row = st * per + group;
+    const bool in = row < p.rows;
+    const int64_t base = row * p.dim;
+    float x[N][V], g[N][V];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * lanes + lane) * V;
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[i][j] = g[i][j] = 0.0f;
+      if (in && c < p.dim) {
+        load<T, V>(static_cast<const T *>(p.x) + base + c, x[i]);
+        load<T, V>(static_cast<const T *>(p.dy) + base + c, g[i]);
+      }
+    }
+    const float mean = in ? p.mean[row] : 0.0f;
+    const float rstd = in ? p.rstd[row] : 0.0f;
+    float su = 0.0f, sux = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * lanes + lane) * V;
+      if (c < p.dim) {
+        float w[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) w[j] = 1.0f;
+        if (p.weight) load_param<V>(p.weight + c, w);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          x[i][j] = (x[i][j] - mean) * rstd;
+          if (p.part) {
+            dw[i][j] = fmaf(g[i][j], x[i][j], dw[i][j]);
+            db[i][j] += g[i][j];
+          }
+          g[i][j] *= w[j];
+          su += g[i][j];
+          sux = fmaf(g[i][j], x[i][j], sux);
+        }
+      }
+    }
+    row_sum2<G>(su, sux, p.wpr, red, slot);
+    su *= inv;
+    sux *= inv;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * lanes + lane) * V;
+      if (in && c < p.dim) {
+        float o[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          o[j] = (g[i][j] - su - x[i][j] * sux) * rstd;
+        if (p.dsum) {
+          float r[V];
+          load<T, V>(static_cast<const T *>(p.dsum) + base + c, r);
+#pragma unroll
+          for (int j = 0; j < V; ++j) o[j] += r[j];
+        }
+        store<T, V>(static_cast<T *>(p.dx) + base + c, o);
+      }
+    }
+    if (FOLD && ++fold == kFold) {
+      fold = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          dw2[i][j] += dw[i][j];
+          db2[i][j] += db[i][j];
+          dw[i][j] = db[i][j] = 0.0f;
+        }
+    }
+  }
+  if (!p.part) return;
+  if (FOLD) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        dw[i][j] += dw2[i][j];
+        db[i][j] += db2[i][j];
+      }
+  }
+  // the block's row groups, in order, into the first one's sums
+  if (group > 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * lanes + lane) * V;
+      if (c < p.dim) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          cols[(int64_t(group - 1) * 2) * p.dim + c + j] = dw[i][j];
+          cols[(int64_t(group - 1) * 2 + 1) * p.dim + c + j] = db[i][j];
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (group == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * lanes + lane) * V;
+      if (c < p.dim) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          for (int k = 0; k + 1 < per; ++k) {
+            dw[i][j] += cols[(int64_t(k) * 2) * p.dim + c + j];
+            db[i][j] += cols[(int64_t(k) * 2 + 1) * p.dim + c + j];
+          }
+          p.part[int64_t(blockIdx.x) * p.dim + c + j] = dw[i][j];
+          p.part[(int64_t(p.parts) + blockIdx.x) * p.dim + c + j] = db[i][j];
+        }
+      }
+    }
+  }
+}
+
+// dweight and dbias from the blocks' partial rows: 32 columns a block, eight
+// warps over the rows, in a fixed order.
+__global__ void __launch_bounds__(256)
+    layernorm_cols_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float red[8][32];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int c = blockIdx.x * 32 + lane;
+  const float *src = p.part + int64_t(blockIdx.y) * p.parts * p.dim;
+  float *dst = blockIdx.y == 0 ? p.dweight : p.dbias;
+  float s = 0.0f;
+  if (c < p.dim)
+#pragma unroll 4
+    for (int r = warp; r < p.parts; r += 8) s += src[int64_t(r) * p.dim + c];
+  red[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < p.dim && dst) {
+    for (int w = 1; w < 8; ++w) s += red[w][lane];
+    dst[c] = s;
+  }
+}
+
+}  // namespace norm
+}  // namespace ssm

@@ -1,0 +1,913 @@
+// Linear attention with a decay for each head, in chunks of 64 steps on the
+// tensor cores, for every supported shape and both activation types.
+//
+// With c_i the sum of the log decays inside the chunk up to step i, S the
+// state in front of it:
+//   y_i = si e^{c_i} q_i S + sp sum_{j <= i} e^{c_i - c_j} (q_i . k_j) v_j
+//   S  <- e^{c_C} S + sw sum_j e^{c_C - c_j} k_j (x) v_j
+// A block of four warps owns one head, one tile of 64 value columns and one
+// segment of a sequence: S stays in float32 registers (each warp a quarter of
+// the key rows), the chunk's q, k, v and a bfloat16 copy of S in shared memory.
+//
+// The backward pass is three such passes. dq_i reads the same states as y_i,
+// transposed: it is linear attention of (query dy, key v, value k). dk and dv
+// run backwards in time: dk is that of (query v, key dy, value q), dv that of
+// (query k, key q, value dy). Counted from the end, step i sits at token
+// t = T - 1 - i, and the decay between two steps is shifted by one: step i
+// carries the log decay of token t + 1.
+//
+// Types. The tensor cores multiply bfloat16 and add float32, so every operand
+// is a sum of bfloat16 planes: x = x0 + x1 + x2, each the rounding of what
+// the ones before leave (8 significant bits each, 24 in all: float32 exactly).
+// bfloat16 inputs are one plane, float32 inputs three. A product of two
+// operands takes the plane pairs (a, b) with a + b < 3; what is left out is
+// below 2^-24 of the product. The state's write takes three planes of the
+// weighted key for both types, so the float32 state has float32 accuracy.
+// Reading the state and the decayed scores takes PS planes: one when only a
+// bfloat16 result comes of them (each then adds a rounding of 2^-9 relative at
+// most half a step, as the result's own rounding does), three for float32
+// results and for the decay's gradient, which sums differences of them.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "device_math.cuh"
+#include "linattn_params.cuh"
+
+namespace ssm {
+namespace la {
+
+using bf16 = __nv_bfloat16;
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const bf16 *p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(p)));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], const bf16 *p) {
+  asm volatile(
+      "ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(smem_u32(p)));
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4],
+                                    uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float lo2(uint32_t v) {
+  return __uint_as_float(v << 16);
+}
+__device__ __forceinline__ float hi2(uint32_t v) {
+  return __uint_as_float(v & 0xffff0000u);
+}
+
+// The first N bfloat16 planes of a pair of floats.
+template <int N>
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[N]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    p[n] = pack2(x, y);
+    x -= lo2(p[n]);
+    y -= hi2(p[n]);
+  }
+}
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
+
+// The log decay of one token and head.
+template <typename T>
+__device__ __forceinline__ double gate_at(const LaParams &p, int64_t b,
+                                          int64_t t, int h) {
+  double g = 0.0;
+  if (p.log_decay)
+    g = double(to_f(static_cast<const T *>(
+        p.log_decay)[(b * p.seqlen + t) * p.heads + h]));
+  if (p.head_log_decay) g += double(p.head_log_decay[h]);
+  return g;
+}
+
+// Where the rows of a chunk come from: row r is step `first + r`.
+struct Rows {
+  int64_t first;  // token of row 0
+  int dir;        // +1, or -1 in reverse
+  int64_t len;    // tokens of this sequence
+  __device__ __forceinline__ int64_t token(int r) const {
+    return first + int64_t(dir) * r;
+  }
+  __device__ __forceinline__ bool live(int r) const { return token(r) < len; }
+};
+
+// One [64][COLS] tile of NP bfloat16 planes from `src` (token 0 of the
+// sequence, at the head's first column); rows past the sequence's length and
+// columns past `cols` are zero whatever the memory holds.
+template <typename T, int NP, int COLS>
+__device__ __forceinline__ void load_tile(bf16 *dst, const T *src,
+                                          int64_t stride, int cols,
+                                          const Rows &rows, bool vec) {
+  constexpr int LD = COLS + 8;
+  constexpr int PER = 8;
+  for (int i = threadIdx.x; i < kLaChunk * (COLS / PER); i += 128) {
+    const int r = i / (COLS / PER), c = (i % (COLS / PER)) * PER;
+    uint32_t pl[NP][4];
+#pragma unroll
+    for (int n = 0; n < NP; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) pl[n][j] = 0u;
+    if (rows.live(r) && c < cols) {
+      const T *s = src + rows.token(r) * stride + c;
+      if constexpr (NP == 1) {
+        if (vec && c + PER <= cols) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4 *>(s));
+          pl[0][0] = v.x; pl[0][1] = v.y; pl[0][2] = v.z; pl[0][3] = v.w;
+        } else {
+          float x[PER];
+#pragma unroll
+          for (int j = 0; j < PER; ++j)
+            x[j] = c + j < cols ? to_f(s[j]) : 0.0f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) pl[0][j] = pack2(x[2 * j], x[2 * j + 1]);
+        }
+      } else {
+        float x[PER];
+        if (vec && c + PER <= cols) {
+          const float4 u = __ldg(reinterpret_cast<const float4 *>(s));
+          const float4 w = __ldg(reinterpret_cast<const float4 *>(s) + 1);
+          x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+          x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < PER; ++j)
+            x[j] = c + j < cols ? to_f(s[j]) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t q[NP];
+          split2<NP>(x[2 * j], x[2 * j + 1], q);
+#pragma unroll
+          for (int n = 0; n < NP; ++n) pl[n][j] = q[n];
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NP; ++n)
+      *reinterpret_cast<uint4 *>(dst + n * kLaChunk * LD + r * LD + c) =
+          make_uint4(pl[n][0], pl[n][1], pl[n][2], pl[n][3]);
+  }
+}
+
+// The chunk's decays, in units of log2. A log decay below -87 makes e^g
+// exactly 0 in float32: such a step starts the state anew, the sums restart
+// there (so that they stay finite and small) and nothing before it is read.
+// The sums are formed in 64 bits and kept as a pair of floats: a difference of
+// two of them is then exact to float32 however much the chunk decays.
+struct Gates {
+  float hi[kLaChunk], lo[kLaChunk];  // c_i since the last restart
+  int from[kLaChunk];                // the last restart at or before step i
+  float read[kLaChunk];              // e^{c_i}, 0 behind a restart
+  float write[kLaChunk];             // e^{c_C - c_i}, 0 before a restart
+  float keep;                        // e^{c_C}, 0 with a restart
+};
+
+// 2^x for a 64-bit x: the float32 rounding of x is put back to first order.
+// What leaves float32's normal numbers is 0, as ex2 has it.
+__device__ __forceinline__ float ex2_d(double x) {
+  if (x < -126.0) return 0.0f;
+  const float hi = float(x);
+  return ex2(hi) * fmaf(float(x - double(hi)), kLn2, 1.0f);
+}
+
+template <typename T>
+__device__ __forceinline__ void load_gates(Gates &g, const LaParams &p,
+                                           const Rows &rows, int64_t b,
+                                           int h, int reverse) {
+  if (threadIdx.x >= 32) return;
+  const int lane = threadIdx.x;
+  double c[2];
+  int from[2];
+  double sum = 0.0;
+  int last = 0;
+  bool any = false;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int r = 2 * lane + j;
+    const int64_t t = rows.token(r) + (reverse ? 1 : 0);
+    double x = 0.0;
+    if (t < rows.len) x = gate_at<T>(p, b, t, h) * 1.4426950408889634;
+    if (x < -126.0) {
+      sum = 0.0;
+      last = r;
+      any = true;
+    } else {
+      sum += x;
+    }
+    c[j] = sum;
+    from[j] = any ? last : -1;
+  }
+  // prefix over the lanes: (sum since the restart, restart or -1)
+  double ps = sum;
+  int pr = any ? last : -1;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const double os = __shfl_up_sync(0xffffffffu, ps, d);
+    const int orr = __shfl_up_sync(0xffffffffu, pr, d);
+    if (lane >= d) {
+      if (pr < 0) {
+        ps += os;
+        pr = orr;
+      }
+    }
+  }
+  double es = __shfl_up_sync(0xffffffffu, ps, 1);
+  int er = __shfl_up_sync(0xffffffffu, pr, 1);
+  if (lane == 0) {
+    es = 0.0;
+    er = -1;
+  }
+  const double end = __shfl_sync(0xffffffffu, ps, 31);
+  const int end_r = __shfl_sync(0xffffffffu, pr, 31);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int r = 2 * lane + j;
+    if (from[j] < 0) {
+      c[j] += es;
+      from[j] = er;
+    }
+    const float hi = float(c[j]);
+    g.hi[r] = hi;
+    g.lo[r] = float(c[j] - double(hi));
+    g.from[r] = from[j] < 0 ? 0 : from[j];
+    g.read[r] = from[j] < 0 ? ex2_d(c[j]) : 0.0f;
+    g.write[r] = r >= end_r ? ex2_d(end - c[j]) : 0.0f;
+  }
+  if (lane == 0) g.keep = end_r < 0 ? ex2_d(end) : 0.0f;
+}
+
+template <typename T, int NP, int PS, int QD, bool STATE_ONLY>
+struct Layout {
+  static constexpr int LDQ = QD + 8, LDV = kLaTile + 8;
+  static constexpr int TQ = kLaChunk * LDQ, TV = kLaChunk * LDV;
+  static constexpr int TS = QD * LDV;
+  static constexpr int K = 0;                       // bf16 offsets
+  static constexpr int V = K + NP * TQ;
+  static constexpr int Q = V + NP * TV;
+  static constexpr int S = Q + (STATE_ONLY ? 0 : NP * TQ);
+  static constexpr int END = S + (STATE_ONLY ? 0 : PS * TS);
+  static constexpr int BYTES = END * 2 + int(sizeof(Gates));
+};
+
+// The state's rows in a warp's accumulators: warp w owns key rows
+// [w QD/4, (w + 1) QD/4) in m-tiles of 16; the usual m16n8 layout.
+template <int QD, class F>
+__device__ __forceinline__ void for_state(F f) {
+  constexpr int MT = QD / 64;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int hrow = 0; hrow < 2; ++hrow)
+        f(m, n, hrow, (warp * MT + m) * 16 + lane / 4 + hrow * 8,
+          n * 8 + (lane % 4) * 2);
+}
+
+// MINB: resident blocks the registers are held to.
+template <typename T, int NP, int PS, int QD, bool STATE_ONLY, int MINB>
+__global__ void __launch_bounds__(128, MINB)
+    linattn_kernel(const __grid_constant__ LaParams p) {
+  using Lay = Layout<T, NP, PS, QD, STATE_ONLY>;
+  constexpr int MT = QD / 64;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  bf16 *sm = reinterpret_cast<bf16 *>(smem_raw);
+  bf16 *Ks = sm + Lay::K, *Vs = sm + Lay::V;
+  bf16 *Qs = sm + Lay::Q, *Ss = sm + Lay::S;
+  Gates &gt = *reinterpret_cast<Gates *>(sm + Lay::END);
+
+  const LaJob &job = p.job[blockIdx.y];
+  // tiles of one head, then heads, are neighbours: they read the same q and k
+  int64_t x = blockIdx.x;
+  const int tile = int(x % job.tiles);
+  x /= job.tiles;
+  const int h = int(x % p.heads);
+  x /= p.heads;
+  const int64_t b = x % p.batch;
+  const int seg = int(x / p.batch);
+  if (seg >= p.nseg) return;
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t L = p.seqlen;
+  int64_t len = L;
+  if (p.lengths) {
+    const int64_t n = p.lengths[b];
+    len = n < 0 ? 0 : n > L ? L : n;
+  }
+  const int64_t total = p.nseg * p.seg_len;
+  const int kh = h / (p.heads / job.k_heads);
+  const int qh = h / (p.heads / job.q_heads);
+  const int vh = h / (p.heads / job.v_heads);
+  const int c0 = tile * kLaTile;
+  const int vcols = min(job.vd - c0, kLaTile);
+  const T *kb = static_cast<const T *>(job.k) + b * L * job.k_stride +
+                int64_t(kh) * job.qd;
+  const T *qb = static_cast<const T *>(job.q) + b * L * job.q_stride +
+                int64_t(qh) * job.qd;
+  const T *vb = static_cast<const T *>(job.v) + b * L * job.v_stride +
+                int64_t(vh) * job.vd + c0;
+  constexpr int VE = 16 / sizeof(T);
+  auto vec_ok = [&](const T *s, int64_t stride) {
+    return (reinterpret_cast<uintptr_t>(s) % 16) == 0 && stride % VE == 0;
+  };
+  const bool kvec = vec_ok(kb, job.k_stride), qvec = vec_ok(qb, job.q_stride),
+             vvec = vec_ok(vb, job.v_stride);
+
+  const int64_t bh = b * p.heads + h;
+  constexpr int64_t SF = int64_t(QD) * kLaTile;
+  float *seg_state =
+      p.nseg > 1 ? job.seg_state +
+                       ((bh * p.nseg + seg) * job.tiles + tile) * SF
+                 : nullptr;
+
+  float S[MT][8][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) S[m][n][j] = 0.0f;
+  if (!STATE_ONLY) {
+    if (p.nseg > 1) {
+      for_state<QD>([&](int m, int n, int hr, int row, int col) {
+        const float2 v = *reinterpret_cast<const float2 *>(
+            seg_state + row * kLaTile + col);
+        S[m][n][2 * hr] = v.x;
+        S[m][n][2 * hr + 1] = v.y;
+      });
+    } else if (job.init) {
+      const float *src = job.init + bh * job.qd * job.vd;
+      for_state<QD>([&](int m, int n, int hr, int row, int col) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (row < job.qd && c0 + col + j < job.vd)
+            S[m][n][2 * hr + j] = src[int64_t(row) * job.state_rs +
+                                      int64_t(c0 + col + j) * job.state_cs];
+      });
+    }
+  }
+
+  float seg_keep = 1.0f;
+  const int chunks = int(p.seg_len / kLaChunk);
+  for (int ch = 0; ch < chunks; ++ch) {
+    Rows rows;
+    const int64_t i0 = int64_t(seg) * p.seg_len + int64_t(ch) * kLaChunk;
+    rows.first = job.reverse ? total - 1 - i0 : i0;
+    rows.dir = job.reverse ? -1 : 1;
+    rows.len = len;
+    const int64_t lowest = job.reverse ? rows.first - (kLaChunk - 1) : i0;
+    const bool idle = lowest >= len;
+    if (idle) {
+      // no live step: the state stays, the rows of y behind the sequence are 0
+      if (!STATE_ONLY && lowest < L) {
+        const int64_t n = L - lowest < kLaChunk ? L - lowest : kLaChunk;
+        for (int64_t i = threadIdx.x; i < n * vcols; i += 128) {
+          const int64_t t = lowest + i / vcols;
+          const int64_t at =
+              ((b * L + t) * p.heads + h) * job.vd + c0 + i % vcols;
+          if (job.y_f32)
+            static_cast<float *>(job.y)[at] = 0.0f;
+          else
+            static_cast<T *>(job.y)[at] = T(0.0f);
+        }
+      }
+      continue;
+    }
+
+    __syncthreads();  // the last chunk's reads are done
+    load_gates<T>(gt, p, rows, b, h, job.reverse);
+    load_tile<T, NP, QD>(Ks, kb, job.k_stride, job.qd, rows, kvec);
+    load_tile<T, NP, kLaTile>(Vs, vb, job.v_stride, vcols, rows, vvec);
+    if constexpr (!STATE_ONLY) {
+      load_tile<T, NP, QD>(Qs, qb, job.q_stride, job.qd, rows, qvec);
+      for_state<QD>([&](int m, int n, int hr, int row, int col) {
+        uint32_t pl[PS];
+        split2<PS>(S[m][n][2 * hr], S[m][n][2 * hr + 1], pl);
+#pragma unroll
+        for (int s = 0; s < PS; ++s)
+          *reinterpret_cast<uint32_t *>(Ss + s * Lay::TS + row * Lay::LDV +
+                                        col) = pl[s];
+      });
+    }
+    __syncthreads();
+
+    if constexpr (!STATE_ONLY) {
+      // ---- scores and the state's part: rows 16 warp .. 16 warp + 15
+      float P[8][4], O[8][4];
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) P[n][j] = O[n][j] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < QD / 16; ++ks) {
+        uint32_t a[NP][4];
+#pragma unroll
+        for (int s = 0; s < NP; ++s)
+          ldsm4(a[s], Qs + s * Lay::TQ + (warp * 16 + lane % 16) * Lay::LDQ +
+                          ks * 16 + (lane / 16) * 8);
+#pragma unroll
+        for (int n2 = 0; n2 < 4; ++n2) {
+          if (n2 <= warp) {
+            uint32_t bk[NP][4];
+#pragma unroll
+            for (int s = 0; s < NP; ++s)
+              ldsm4(bk[s], Ks + s * Lay::TQ +
+                               (n2 * 16 + lane % 8 + (lane / 16) * 8) *
+                                   Lay::LDQ +
+                               ks * 16 + ((lane / 8) % 2) * 8);
+#pragma unroll
+            for (int s = 0; s < NP; ++s)
+#pragma unroll
+              for (int u = 0; u < NP; ++u)
+                if (s + u < 3) {
+                  mma(P[2 * n2], a[s], bk[u][0], bk[u][1]);
+                  mma(P[2 * n2 + 1], a[s], bk[u][2], bk[u][3]);
+                }
+          }
+        }
+#pragma unroll
+        for (int n2 = 0; n2 < 4; ++n2) {
+          uint32_t bs[PS][4];
+#pragma unroll
+          for (int s = 0; s < PS; ++s)
+            ldsm4t(bs[s], Ss + s * Lay::TS +
+                              (ks * 16 + lane % 16) * Lay::LDV + n2 * 16 +
+                              (lane / 16) * 8);
+#pragma unroll
+          for (int s = 0; s < NP; ++s)
+#pragma unroll
+            for (int u = 0; u < PS; ++u)
+              if (s + u < 3) {
+                mma(O[2 * n2], a[s], bs[u][0], bs[u][1]);
+                mma(O[2 * n2 + 1], a[s], bs[u][2], bs[u][3]);
+              }
+        }
+      }
+      // ---- decay: rows r0 and r0 + 8 of this lane
+      const int r0 = warp * 16 + lane / 4;
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        const int r = r0 + 8 * hr;
+        const float rd = gt.read[r] * job.si;
+        const float chi = gt.hi[r], clo = gt.lo[r];
+        const int from = gt.from[r];
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          // a restart forgets the state whatever it held
+          O[n][2 * hr] = rd == 0.0f ? 0.0f : O[n][2 * hr] * rd;
+          O[n][2 * hr + 1] = rd == 0.0f ? 0.0f : O[n][2 * hr + 1] * rd;
+          if (n < 2 * warp + 2) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int c = n * 8 + (lane % 4) * 2 + j;
+              const float d =
+                  ex2((chi - gt.hi[c]) + (clo - gt.lo[c])) * job.sp;
+              P[n][2 * hr + j] =
+                  (c <= r && c >= from) ? P[n][2 * hr + j] * d : 0.0f;
+            }
+          }
+        }
+      }
+      // ---- scores times values
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        if (kk <= warp) {
+          uint32_t a[PS][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t pl[PS];
+            split2<PS>(P[2 * kk + i / 2][2 * (i % 2)],
+                       P[2 * kk + i / 2][2 * (i % 2) + 1], pl);
+#pragma unroll
+            for (int s = 0; s < PS; ++s) a[s][i] = pl[s];
+          }
+#pragma unroll
+          for (int n2 = 0; n2 < 4; ++n2) {
+            uint32_t bv[NP][4];
+#pragma unroll
+            for (int s = 0; s < NP; ++s)
+              ldsm4t(bv[s], Vs + s * Lay::TV +
+                                (kk * 16 + lane % 16) * Lay::LDV + n2 * 16 +
+                                (lane / 16) * 8);
+#pragma unroll
+            for (int s = 0; s < PS; ++s)
+#pragma unroll
+              for (int u = 0; u < NP; ++u)
+                if (s + u < 3) {
+                  mma(O[2 * n2], a[s], bv[u][0], bv[u][1]);
+                  mma(O[2 * n2 + 1], a[s], bv[u][2], bv[u][3]);
+                }
+          }
+        }
+      }
+      // ---- y, and the row dots the decay's gradient is made of
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        const int r = r0 + 8 * hr;
+        const int64_t t = rows.token(r);
+        const bool in = t < L, live = t < len;
+        float dot = 0.0f;
+        if (in) {
+          const int64_t at = ((b * L + t) * p.heads + h) * job.vd + c0;
+          const T *ds =
+              job.dot ? static_cast<const T *>(job.dot) +
+                            (b * L + t) * job.dot_stride +
+                            int64_t(h / (p.heads / job.dot_heads)) * job.vd +
+                            c0
+                      : nullptr;
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            const int c = n * 8 + (lane % 4) * 2;
+            const float v0 = live ? O[n][2 * hr] : 0.0f;
+            const float v1 = live ? O[n][2 * hr + 1] : 0.0f;
+            if (job.y_f32) {
+              float *y = static_cast<float *>(job.y) + at + c;
+              if (c + 1 < vcols && job.vd % 2 == 0) {
+                *reinterpret_cast<float2 *>(y) = make_float2(v0, v1);
+              } else {
+                if (c < vcols) y[0] = v0;
+                if (c + 1 < vcols) y[1] = v1;
+              }
+            } else {
+              T *y = static_cast<T *>(job.y) + at + c;
+              if (c + 1 < vcols && job.vd % 2 == 0) {
+                if constexpr (sizeof(T) == 2)
+                  *reinterpret_cast<uint32_t *>(y) = pack2(v0, v1);
+                else
+                  *reinterpret_cast<float2 *>(y) = make_float2(v0, v1);
+              } else {
+                if (c < vcols) y[0] = T(v0);
+                if (c + 1 < vcols) y[1] = T(v1);
+              }
+            }
+            if (ds && live) {
+              if (c < vcols) dot += v0 * to_f(ds[c]);
+              if (c + 1 < vcols) dot += v1 * to_f(ds[c + 1]);
+            }
+          }
+        }
+        if (job.rows) {
+          dot += __shfl_xor_sync(0xffffffffu, dot, 1);
+          dot += __shfl_xor_sync(0xffffffffu, dot, 2);
+          if (in && lane % 4 == 0)
+            job.rows[((int64_t(tile) * p.batch + b) * p.heads + h) * L + t] =
+                dot;
+        }
+      }
+    }
+
+    // ---- the state: S <- keep S + (weighted k)^T v
+    const float keep = gt.keep;
+    seg_keep *= keep;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          S[m][n][j] = keep == 0.0f ? 0.0f : S[m][n][j] * keep;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      float w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = gt.write[kk * 16 + (lane % 4) * 2 + (j / 2) * 8 + j % 2] *
+               job.sw;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        uint32_t kr[NP][4], a[3][4];
+#pragma unroll
+        for (int s = 0; s < NP; ++s)
+          ldsm4t(kr[s], Ks + s * Lay::TQ +
+                            (kk * 16 + lane % 8 + (lane / 16) * 8) * Lay::LDQ +
+                            (warp * MT + m) * 16 + ((lane / 8) % 2) * 8);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float f0 = 0.0f, f1 = 0.0f;
+#pragma unroll
+          for (int s = NP - 1; s >= 0; --s) {
+            f0 += lo2(kr[s][i]);
+            f1 += hi2(kr[s][i]);
+          }
+          uint32_t pl[3];
+          split2<3>(f0 * w[(i / 2) * 2], f1 * w[(i / 2) * 2 + 1], pl);
+#pragma unroll
+          for (int s = 0; s < 3; ++s) a[s][i] = pl[s];
+        }
+#pragma unroll
+        for (int n2 = 0; n2 < 4; ++n2) {
+          uint32_t bv[NP][4];
+#pragma unroll
+          for (int s = 0; s < NP; ++s)
+            ldsm4t(bv[s], Vs + s * Lay::TV +
+                              (kk * 16 + lane % 16) * Lay::LDV + n2 * 16 +
+                              (lane / 16) * 8);
+#pragma unroll
+          for (int s = 0; s < 3; ++s)
+#pragma unroll
+            for (int u = 0; u < NP; ++u)
+              if (s + u < 3) {
+                mma(S[m][2 * n2], a[s], bv[u][0], bv[u][1]);
+                mma(S[m][2 * n2 + 1], a[s], bv[u][2], bv[u][3]);
+              }
+        }
+      }
+    }
+  }
+
+  if constexpr (STATE_ONLY) {
+    for_state<QD>([&](int m, int n, int hr, int row, int col) {
+      *reinterpret_cast<float2 *>(seg_state + row * kLaTile + col) =
+          make_float2(S[m][n][2 * hr], S[m][n][2 * hr + 1]);
+    });
+    if (tile == 0 && threadIdx.x == 0)
+      job.seg_decay[bh * p.nseg + seg] = seg_keep;
+  } else if (job.last && seg == p.nseg - 1) {
+    // running backwards, the first token's own decay is still to come
+    float f = 1.0f;
+    if (job.reverse && len > 0)
+      f = ex2_d(gate_at<T>(p, b, 0, h) * 1.4426950408889634);
+    float *dst = job.last + bh * job.qd * job.vd;
+    for_state<QD>([&](int m, int n, int hr, int row, int col) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (row < job.qd && c0 + col + j < job.vd)
+          dst[int64_t(row) * job.state_rs +
+              int64_t(c0 + col + j) * job.state_cs] =
+              f == 0.0f ? 0.0f : S[m][n][2 * hr + j] * f;
+    });
+  }
+}
+
+// The states in front of the segments, from what each segment adds on its own:
+// S_{m+1} = decay_m S_m + U_m, in place (entry m takes S_m; the last segment's
+// own part is not formed here). One thread per state element.
+template <int QD>
+__global__ void __launch_bounds__(256)
+    linattn_join_kernel(const __grid_constant__ LaParams p) {
+  const LaJob &job = p.job[blockIdx.y];
+  constexpr int64_t SF = int64_t(QD) * kLaTile;
+  const int64_t per = SF * job.tiles;
+  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (e >= per * p.batch * p.heads) return;
+  const int64_t bh = e / per, el = e % per;
+  const int tile = int(el / SF), row = int(el % SF / kLaTile),
+            col = int(el % kLaTile) + tile * kLaTile;
+  float S = 0.0f;
+  if (job.init && row < job.qd && col < job.vd)
+    S = job.init[bh * job.qd * job.vd + int64_t(row) * job.state_rs +
+                 int64_t(col) * job.state_cs];
+  float *u = job.seg_state + bh * p.nseg * per + el;
+  const float *d = job.seg_decay + bh * p.nseg;
+  int m = 0;
+  const int n = p.nseg - 1;
+  for (; m + 4 <= n; m += 4) {
+    float a[4], k[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      a[j] = u[(m + j) * per];
+      k[j] = d[m + j];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u[(m + j) * per] = S;
+      S = k[j] == 0.0f ? a[j] : fmaf(k[j], S, a[j]);
+    }
+  }
+  for (; m < n; ++m) {
+    const float a = u[m * per];
+    u[m * per] = S;
+    S = d[m] == 0.0f ? a : fmaf(d[m], S, a);
+  }
+  u[n * per] = S;
+}
+
+__device__ __forceinline__ float block_sum(float v, float *red) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
+  __syncthreads();
+  float s = 0.0f;
+  for (int w = 0; w < int(blockDim.x) / 32; ++w) s += red[w];
+  __syncthreads();
+  return s;
+}
+
+// The log decay's gradient. With G the gradient of the state,
+//   dg_t = <a_t S_{t-1}, G_t> = dg_{t+1} + q_t . dq_t - k_t . dk_t,
+// summed backwards inside each segment from its end, where the product of the
+// state and its gradient is formed from the two passes' segment states: the
+// differences are then never summed over more than one segment. One block
+// per (sequence, head, segment).
+template <typename T>
+__global__ void __launch_bounds__(256)
+    linattn_gate_kernel(const __grid_constant__ LaGateParams p) {
+  __shared__ float red[8];
+  __shared__ float warp_tot[8];
+  const int64_t x = blockIdx.x;
+  const int seg = int(x % p.nseg);
+  const int64_t bh = x / p.nseg;
+  const int64_t b = bh / p.heads;
+  const int h = int(bh % p.heads);
+  const int64_t L = p.seqlen;
+  int64_t len = L;
+  if (p.lengths) {
+    const int64_t n = p.lengths[b];
+    len = n < 0 ? 0 : n > L ? L : n;
+  }
+  const int64_t t0 = int64_t(seg) * p.seg_len;
+  const int64_t t1 = t0 + p.seg_len;
+  // the product of the state behind the segment and its gradient
+  const float *S = nullptr, *G = nullptr;
+  int64_t n = 0;
+  float end = 0.0f;
+  if (t1 < len) {
+    S = p.fwd_state + (bh * p.nseg + seg + 1) * p.state_floats;
+    G = p.rev_state + (bh * p.nseg + p.nseg - 1 - seg) * p.state_floats;
+    n = p.state_floats;
+  } else if (p.dh_last) {
+    S = p.last_state + bh * p.last_floats;
+    G = p.dh_last + bh * p.last_floats;
+    n = p.last_floats;
+  }
+  if (n) {
+    float s = 0.0f;
+    for (int64_t i = threadIdx.x; i < n; i += 256) s = fmaf(S[i], G[i], s);
+    end = block_sum(s, red);
+    if (t1 < len) {  // the decay of the next segment's first token
+      double g = 0.0;
+      if (p.log_decay)
+        g = double(to_f(
+            static_cast<const T *>(p.log_decay)[(b * L + t1) * p.heads + h]));
+      if (p.head_log_decay) g += double(p.head_log_decay[h]);
+      const float a = ex2_d(g * 1.4426950408889634);
+      end = a == 0.0f ? 0.0f : end * a;
+    }
+  }
+  // backwards, 256 tokens at a time: thread i has the i-th token from the end
+  float carry = end, part = 0.0f;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  for (int64_t hi = t1; hi > t0; hi -= 256) {
+    const int64_t t = hi - 1 - threadIdx.x;
+    float v = 0.0f;
+    if (t >= t0 && t < len)
+      for (int k = 0; k < p.tiles; ++k) {
+        const int64_t at = ((int64_t(k) * p.batch + b) * p.heads + h) * L + t;
+        v += p.rows_q[at] - p.rows_k[at];
+      }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const float o = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += o;
+    }
+    if (lane == 31) warp_tot[warp] = v;
+    __syncthreads();
+    float before = carry;
+    for (int w = 0; w < warp; ++w) before += warp_tot[w];
+    v += before;
+    for (int w = 0; w < 8; ++w) carry += warp_tot[w];
+    __syncthreads();
+    if (t >= t0 && t < L) {
+      const float out = t < len ? v : 0.0f;
+      if (p.dlog_decay)
+        static_cast<T *>(p.dlog_decay)[(b * L + t) * p.heads + h] = T(out);
+      part += out;
+    }
+  }
+  if (p.part) {
+    part = block_sum(part, red);
+    if (threadIdx.x == 0) p.part[(b * p.nseg + seg) * p.heads + h] = part;
+  }
+}
+
+// out[h] = sum over n rows of part[n][heads], in a fixed order.
+__global__ void __launch_bounds__(128)
+    linattn_head_sum_kernel(const float *part, int64_t n, int heads,
+                            float *out) {
+  __shared__ double red[4];
+  const int h = blockIdx.x;
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < n; i += 128)
+    s += double(part[i * heads + h]);
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) out[h] = float(red[0] + red[1] + red[2] + red[3]);
+}
+
+// The gradient of a shared head: out[r][g][d] = sum of the group's heads, in
+// order, of part[r][h][d].
+template <typename T>
+__global__ void __launch_bounds__(256)
+    linattn_group_sum_kernel(const float *part, int64_t rows, int groups,
+                             int per, int d, T *out) {
+  const int64_t n = rows * groups * d;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n;
+       i += int64_t(gridDim.x) * 256) {
+    const int64_t rg = i / d;
+    const int c = int(i % d);
+    float s = 0.0f;
+    for (int k = 0; k < per; ++k) s += part[(rg * per + k) * d + c];
+    out[i] = T(s);
+  }
+}
+
+// ---- one token: S <- a S + k (x) v in place, y = scale q S.
+// Bound by the state's bytes (read and written once). A block of 8 warps owns
+// one head and 32 W value columns; each warp takes every eighth key row, a
+// lane W columns of it, and the rows' parts of y are added through shared
+// memory in a fixed order.
+template <typename T, int W>
+__global__ void __launch_bounds__(256)
+    linattn_step_kernel(const __grid_constant__ LaStepParams p) {
+  __shared__ float ks[kLaMaxKey], qs[kLaMaxKey];
+  __shared__ float part[8][32 * W];
+  const int tiles = (p.dv + 32 * W - 1) / (32 * W);
+  const int tile = int(blockIdx.x % tiles);
+  const int64_t bh = blockIdx.x / tiles;
+  const int64_t b = bh / p.heads;
+  const int h = int(bh % p.heads), g = h / (p.heads / p.groups);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int c0 = tile * 32 * W + lane * W;
+  float *S = p.state + bh * p.dk * p.dv + c0;
+  const T *kp = static_cast<const T *>(p.k) + b * p.k_stride + g * p.dk;
+  const T *qp = static_cast<const T *>(p.q) + b * p.q_stride + g * p.dk;
+  const T *vp = static_cast<const T *>(p.v) + b * p.v_stride + h * p.dv + c0;
+  for (int i = threadIdx.x; i < p.dk; i += 256) {
+    ks[i] = to_f(kp[i]);
+    qs[i] = to_f(qp[i]);
+  }
+  double gd = 0.0;
+  if (p.log_decay)
+    gd = double(to_f(static_cast<const T *>(p.log_decay)[bh]));
+  if (p.head_log_decay) gd += double(p.head_log_decay[h]);
+  const float a = ex2_d(gd * 1.4426950408889634);
+  float v[W], y[W];
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+    v[j] = c0 + j < p.dv ? to_f(vp[j]) : 0.0f;
+    y[j] = 0.0f;
+  }
+  __syncthreads();
+  if (c0 < p.dv) {
+#pragma unroll 4
+    for (int r = warp; r < p.dk; r += 8) {
+      float *s = S + int64_t(r) * p.dv;
+      float x[W];
+      if constexpr (W == 4) {
+        const float4 u = *reinterpret_cast<const float4 *>(s);
+        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+      } else {
+        x[0] = s[0];
+      }
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        // a = 0 starts anew, whatever the state held
+        x[j] = a == 0.0f ? ks[r] * v[j] : fmaf(a, x[j], ks[r] * v[j]);
+        y[j] = fmaf(qs[r], x[j], y[j]);
+      }
+      if constexpr (W == 4)
+        *reinterpret_cast<float4 *>(s) = make_float4(x[0], x[1], x[2], x[3]);
+      else
+        s[0] = x[0];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < W; ++j) part[warp][lane * W + j] = y[j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * W; i += 256) {
+    const int c = tile * 32 * W + i;
+    if (c < p.dv) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) s += part[w][i];
+      static_cast<T *>(p.y)[bh * p.dv + c] = T(s * p.scale);
+    }
+  }
+}
+
+}  // namespace la
+}  // namespace ssm

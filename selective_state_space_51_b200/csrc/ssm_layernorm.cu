@@ -1,0 +1,237 @@
+// C ABI of the layer-norm entry points: host-side validation, the choice of
+// the row layout and launches. The contract is in include/ssm_layernorm.h.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "../../include/ssm_layernorm.h"
+#include "device_info.cuh"
+#include "kernel_layernorm.cuh"
+
+namespace {
+
+using ssm::aligned;
+using ssm::NormParams;
+using bf16 = __nv_bfloat16;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// How a row is spread: G lanes (short rows) or wpr warps, n groups a thread.
+struct Shape {
+  int g = 32, wpr = 1, n = 1;
+  int threads = 256, per = 1;  // of a block; rows of a block
+};
+
+// `most`: groups of V elements a thread may hold.
+Shape shape_of(int dim, int v, int most) {
+  Shape s;
+  const int nv = int(ceil_div(dim, v));
+  if (nv <= 16) {
+    s.g = nv <= 4 ? 4 : nv <= 8 ? 8 : 16;
+  } else {
+    s.wpr = int(ceil_div(nv, 32 * most));
+    s.n = int(ceil_div(nv, 32 * s.wpr));
+  }
+  const int lanes = s.g < 32 ? s.g : 32 * s.wpr;
+  s.per = std::max(1, 256 / lanes);
+  s.threads = lanes * s.per;
+  return s;
+}
+
+// Blocks the backward pass runs on (and partial rows it leaves): what is
+// resident at once, or one for each step of rows if there are fewer.
+int parts_of(const Shape &s, int64_t rows, int sms) {
+  const int per_sm = std::max(1, 1024 / s.threads);
+  return int(std::min<int64_t>(ceil_div(rows, s.per), int64_t(sms) * per_sm));
+}
+
+// Groups a thread may hold: 16 elements (32 in the forward pass with
+// bfloat16). The widest row then takes 16 warps, the launch bound.
+int most_groups(int v, bool bwd) { return v == 8 && !bwd ? 4 : 16 / v; }
+
+template <typename T, int V, int N, int G>
+int launch_fwd(const NormParams &p, const Shape &s, int sms, cudaStream_t st) {
+  const int64_t steps = ceil_div(p.rows, s.per);
+  const int64_t grid = std::min<int64_t>(steps, int64_t(sms) * 64);
+  ssm::norm::layernorm_fwd_kernel<T, V, N, G>
+      <<<unsigned(grid), s.threads, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
+}
+
+template <typename T, int V, int N, int G>
+int launch_bwd(const NormParams &p, const Shape &s, cudaStream_t st) {
+  auto kern = ssm::norm::layernorm_bwd_kernel<T, V, N, G>;
+  const size_t smem =
+      p.part ? size_t(s.per - 1) * 2 * p.dim * sizeof(float) : 0;
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           int(smem)) != cudaSuccess) {
+    cudaGetLastError();
+    return SSM_ERR_CUDA;
+  }
+  kern<<<unsigned(p.parts), s.threads, smem, st>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return SSM_ERR_CUDA;
+  if (!p.part) return SSM_OK;
+  ssm::norm::layernorm_cols_kernel<<<dim3(unsigned(ceil_div(p.dim, 32)), 2),
+                                     256, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
+}
+
+template <typename T, int V, bool BWD, int N, int G>
+int launch(const NormParams &p, const Shape &s, int sms, cudaStream_t st) {
+  if constexpr (BWD) return launch_bwd<T, V, N, G>(p, s, st);
+  else return launch_fwd<T, V, N, G>(p, s, sms, st);
+}
+
+template <typename T, int V, bool BWD>
+int pick(const NormParams &p, const Shape &s, int sms, cudaStream_t st) {
+  if (s.g == 4) return launch<T, V, BWD, 1, 4>(p, s, sms, st);
+  if (s.g == 8) return launch<T, V, BWD, 1, 8>(p, s, sms, st);
+  if (s.g == 16) return launch<T, V, BWD, 1, 16>(p, s, sms, st);
+  if (s.n == 1) return launch<T, V, BWD, 1, 32>(p, s, sms, st);
+  if (s.n == 2) return launch<T, V, BWD, 2, 32>(p, s, sms, st);
+  if constexpr (V < 8 || !BWD) {
+    if (s.n <= 3) return launch<T, V, BWD, 3, 32>(p, s, sms, st);
+    if (s.n <= 4) return launch<T, V, BWD, 4, 32>(p, s, sms, st);
+  }
+  if constexpr (V == 1) {
+    if (s.n <= 8) return launch<T, V, BWD, 8, 32>(p, s, sms, st);
+    return launch<T, V, BWD, 16, 32>(p, s, sms, st);
+  }
+  return SSM_ERR_UNSUPPORTED;
+}
+
+int run(const NormParams &p, bool wide, bool bwd, int dtype, const Shape &s,
+        int sms, cudaStream_t st) {
+  if (dtype == SSM_F32) {
+    if (wide)
+      return bwd ? pick<float, 4, true>(p, s, sms, st)
+                 : pick<float, 4, false>(p, s, sms, st);
+    return bwd ? pick<float, 1, true>(p, s, sms, st)
+               : pick<float, 1, false>(p, s, sms, st);
+  }
+  if (wide)
+    return bwd ? pick<bf16, 8, true>(p, s, sms, st)
+               : pick<bf16, 8, false>(p, s, sms, st);
+  return bwd ? pick<bf16, 1, true>(p, s, sms, st)
+             : pick<bf16, 1, false>(p, s, sms, st);
+}
+
+int check(int64_t rows, int64_t dim, int dtype) {
+  if (rows <= 0 || dim <= 0) return SSM_ERR_INVALID;
+  if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_UNSUPPORTED;
+  if (dim > SSM_LAYERNORM_MAX_DIM) return SSM_ERR_UNSUPPORTED;
+  if (rows > (int64_t(1) << 42)) return SSM_ERR_INVALID;
+  return SSM_OK;
+}
+
+// Whether rows move in 16-byte groups: every row starts on a 16-byte boundary
+// and so do the parameters' groups.
+bool wide_rows(int64_t dim, size_t esz,
+               std::initializer_list<const void *> list) {
+  if (dim * esz % 16 != 0) return false;
+  for (const void *q : list)
+    if (q && !aligned(q, 16)) return false;
+  return true;
+}
+
+int width(bool wide, size_t esz) { return wide ? int(16 / esz) : 1; }
+
+// The backward pass's layout: the widest of what alignment may leave it.
+Shape bwd_shape(int64_t dim, bool wide, size_t esz) {
+  const int v = width(wide, esz);
+  return shape_of(int(dim), v, most_groups(v, true));
+}
+
+}  // namespace
+
+extern "C" {
+
+int ssm_layernorm_workspace(int device, int64_t rows, int64_t dim, int dtype,
+                            size_t *bytes) {
+  if (!bytes) return SSM_ERR_INVALID;
+  *bytes = 0;
+  int rc = check(rows, dim, dtype);
+  if (rc != SSM_OK) return rc;
+  int sms = 0;
+  rc = ssm::device_sms(device, &sms);
+  if (rc != SSM_OK) return rc;
+  const size_t esz = dtype == SSM_F32 ? 4 : 2;
+  int parts = parts_of(bwd_shape(dim, false, esz), rows, sms);
+  if (dim * esz % 16 == 0)
+    parts = std::max(parts, parts_of(bwd_shape(dim, true, esz), rows, sms));
+  *bytes = size_t(parts) * 2 * dim * sizeof(float);
+  return SSM_OK;
+}
+
+int ssm_layernorm_fwd(int device, const void *x, const void *residual,
+                      const float *weight, const float *bias, float eps,
+                      void *y, void *sum, float *mean, float *rstd,
+                      int64_t rows, int64_t dim, int dtype,
+                      struct CUstream_st *stream) {
+  if (!x || !y || (sum && !residual)) return SSM_ERR_INVALID;
+  int rc = check(rows, dim, dtype);
+  if (rc != SSM_OK) return rc;
+  const size_t esz = dtype == SSM_F32 ? 4 : 2;
+  for (const void *q : {x, residual, static_cast<const void *>(y),
+                        static_cast<const void *>(sum)})
+    if (q && !aligned(q, esz)) return SSM_ERR_ALIGN;
+  for (const float *q : {weight, bias, static_cast<const float *>(mean),
+                         static_cast<const float *>(rstd)})
+    if (q && !aligned(q, 4)) return SSM_ERR_ALIGN;
+  int sms = 0;
+  rc = ssm::device_ready(device, &sms);
+  if (rc != SSM_OK) return rc;
+  NormParams p{};
+  p.x = x; p.residual = residual; p.weight = weight; p.bias = bias;
+  p.y = y; p.sum = sum; p.mean = mean; p.rstd = rstd; p.eps = eps;
+  p.rows = rows; p.dim = int(dim);
+  const bool wide = wide_rows(dim, esz, {x, residual, y, sum, weight, bias});
+  const int v = width(wide, esz);
+  const Shape s = shape_of(p.dim, v, most_groups(v, false));
+  p.wpr = s.wpr;
+  return run(p, wide, false, dtype, s, sms,
+             reinterpret_cast<cudaStream_t>(stream));
+}
+
+int ssm_layernorm_bwd(int device, const void *dy, const void *x,
+                      const float *mean, const float *rstd,
+                      const float *weight, const void *dsum, void *dx,
+                      float *dweight, float *dbias, void *workspace,
+                      size_t workspace_bytes, int64_t rows, int64_t dim,
+                      int dtype, struct CUstream_st *stream) {
+  if (!dy || !x || !mean || !rstd || !dx) return SSM_ERR_INVALID;
+  int rc = check(rows, dim, dtype);
+  if (rc != SSM_OK) return rc;
+  const size_t esz = dtype == SSM_F32 ? 4 : 2;
+  for (const void *q : {dy, x, dsum, static_cast<const void *>(dx)})
+    if (q && !aligned(q, esz)) return SSM_ERR_ALIGN;
+  for (const float *q :
+       {mean, rstd, weight, static_cast<const float *>(dweight),
+        static_cast<const float *>(dbias)})
+    if (q && !aligned(q, 4)) return SSM_ERR_ALIGN;
+  int sms = 0;
+  rc = ssm::device_ready(device, &sms);
+  if (rc != SSM_OK) return rc;
+  NormParams p{};
+  p.x = x; p.dy = dy; p.dsum = dsum; p.dx = dx; p.weight = weight;
+  p.mean = const_cast<float *>(mean); p.rstd = const_cast<float *>(rstd);
+  p.dweight = dweight; p.dbias = dbias;
+  p.rows = rows; p.dim = int(dim);
+  const bool wide = wide_rows(dim, esz, {dy, x, dsum, dx, weight});
+  const Shape s = bwd_shape(dim, wide, esz);
+  p.wpr = s.wpr;
+  p.parts = parts_of(s, rows, sms);
+  if (dweight || dbias) {
+    if (!workspace ||
+        workspace_bytes < size_t(p.parts) * 2 * dim * sizeof(float))
+      return SSM_ERR_INVALID;
+    if (!aligned(workspace, 4)) return SSM_ERR_ALIGN;
+    p.part = static_cast<float *>(workspace);
+  }
+  return run(p, wide, true, dtype, s, sms,
+             reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

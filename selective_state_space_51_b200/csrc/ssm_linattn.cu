@@ -1,0 +1,461 @@
+// C ABI of the linear-attention entry points: host-side validation, the split
+// of long sequences, workspaces and launches. The contract is in
+// include/ssm_linattn.h.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "../../include/ssm_linattn.h"
+#include "device_info.cuh"
+#include "kernel_linattn.cuh"
+
+namespace {
+
+using ssm::aligned;
+using ssm::LaGateParams;
+using ssm::LaJob;
+using ssm::LaParams;
+using ssm::LaStepParams;
+using bf16 = __nv_bfloat16;
+
+constexpr int64_t kMaxElements = int64_t(1) << 56;
+// The decay's gradient sums differences inside a segment: a bounded segment
+// bounds how many of them are added up.
+constexpr int64_t kGateSegment = 1024;
+// Shortest segment a sequence is split into: the state a segment hands over
+// is worth about two chunks' bytes.
+constexpr int64_t kMinSegment = 256;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int key_pad(int64_t d) { return d <= 64 ? 64 : 128; }
+
+// Checks shared by every entry; fills dense strides in.
+int check_dims(ssm_linattn_dims *d, int dtype, int64_t max_value) {
+  if (d->batch <= 0 || d->seqlen <= 0 || d->heads <= 0 || d->groups <= 0 ||
+      d->dk <= 0 || d->dv <= 0 || d->heads % d->groups != 0)
+    return SSM_ERR_INVALID;
+  if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_UNSUPPORTED;
+  if (d->dk > ssm::kLaMaxKey || d->dv > max_value || d->heads > (1 << 20))
+    return SSM_ERR_UNSUPPORTED;
+  if (d->q_stride == 0) d->q_stride = d->groups * d->dk;
+  if (d->k_stride == 0) d->k_stride = d->groups * d->dk;
+  if (d->v_stride == 0) d->v_stride = d->heads * d->dv;
+  if (d->q_stride < d->groups * d->dk || d->k_stride < d->groups * d->dk ||
+      d->v_stride < d->heads * d->dv)
+    return SSM_ERR_INVALID;
+  int64_t rows = 0, n = 0, st = 0;
+  if (__builtin_mul_overflow(d->batch, d->seqlen, &rows) ||
+      rows > kMaxElements)
+    return SSM_ERR_INVALID;
+  for (int64_t s : {d->q_stride, d->k_stride, d->v_stride, d->heads * d->dk})
+    if (__builtin_mul_overflow(rows, s, &n) || n > kMaxElements)
+      return SSM_ERR_INVALID;
+  if (__builtin_mul_overflow(d->batch * d->heads, d->dk * d->dv, &st) ||
+      st > kMaxElements)
+    return SSM_ERR_INVALID;
+  return SSM_OK;
+}
+
+struct Plan {
+  int nseg = 1;
+  int64_t seg_len = 0;
+  // byte offsets into the workspace; jobs: y or dq, dk, dv
+  size_t state[3] = {0, 0, 0}, decay[3] = {0, 0, 0};
+  size_t part_dq = 0, part_dk = 0, rows_q = 0, rows_k = 0, part_head = 0,
+         last = 0;
+  size_t bytes = 0;
+};
+
+size_t take(size_t *at, size_t floats) {
+  const size_t here = *at;
+  *at += (floats * sizeof(float) + 255) / 256 * 256;
+  return here;
+}
+
+// Segments: where one block for each sequence, head and tile leaves over half
+// of the GPU idle, a sequence is cut so that about `per_sm` blocks are there
+// for each SM. The states in front of the segments cost one more reading of k
+// and v, so a grid that fills the GPU by itself is not cut.
+void cut(Plan *pl, int64_t blocks, int64_t L, int sms, int per_sm,
+         int64_t most) {
+  const int64_t slots = int64_t(sms) * per_sm;
+  int64_t n = 1;
+  if (blocks * 2 <= slots)
+    n = std::min(slots / blocks, std::max<int64_t>(1, L / kMinSegment));
+  n = std::max(n, ceil_div(L, most));
+  const int64_t chunks = ceil_div(L, ssm::kLaChunk);
+  const int64_t per = ceil_div(chunks, n);
+  pl->seg_len = per * ssm::kLaChunk;
+  pl->nseg = int(ceil_div(chunks, per));
+}
+
+int resident(int dtype) { return dtype == SSM_BF16 ? 3 : 2; }
+
+Plan plan_fwd(const ssm_linattn_dims &d, int dtype, int sms) {
+  Plan pl;
+  const int64_t tiles = ceil_div(d.dv, ssm::kLaTile);
+  cut(&pl, d.batch * d.heads * tiles, d.seqlen, sms, resident(dtype),
+      int64_t(1) << 40);
+  if (pl.nseg > 1) {
+    const size_t bh = size_t(d.batch) * d.heads;
+    pl.state[0] = take(&pl.bytes, bh * pl.nseg * tiles * key_pad(d.dk) *
+                                      ssm::kLaTile);
+    pl.decay[0] = take(&pl.bytes, bh * pl.nseg);
+  }
+  return pl;
+}
+
+Plan plan_bwd(const ssm_linattn_dims &d, int dtype, bool gate, int sms) {
+  Plan pl;
+  const int64_t tk = ceil_div(d.dk, ssm::kLaTile),
+                tv = ceil_div(d.dv, ssm::kLaTile);
+  const size_t bh = size_t(d.batch) * d.heads;
+  cut(&pl, d.batch * d.heads * (2 * tk + tv), d.seqlen, sms, resident(dtype),
+      gate ? kGateSegment : int64_t(1) << 40);
+  if (pl.nseg > 1)
+    for (int j = 0; j < 3; ++j) {
+      pl.state[j] = take(&pl.bytes, bh * pl.nseg * (j < 2 ? tk : tv) *
+                                        key_pad(j < 2 ? d.dv : d.dk) *
+                                        ssm::kLaTile);
+      pl.decay[j] = take(&pl.bytes, bh * pl.nseg);
+    }
+  if (d.groups != d.heads) {
+    pl.part_dq = take(&pl.bytes, bh * d.seqlen * d.dk);
+    pl.part_dk = take(&pl.bytes, bh * d.seqlen * d.dk);
+  }
+  if (gate) {
+    pl.rows_q = take(&pl.bytes, bh * d.seqlen * tk);
+    pl.rows_k = take(&pl.bytes, bh * d.seqlen * tk);
+    pl.part_head = take(&pl.bytes, bh * pl.nseg);
+    pl.last = take(&pl.bytes, bh * d.dk * d.dv);
+  }
+  return pl;
+}
+
+// Every job of `p` (n of them), which share QD and PS.
+template <typename T, int NP, int PS, int QD>
+int launch_jobs(const LaParams &p, int n, cudaStream_t s) {
+  constexpr int MINB = NP == 3 ? (QD == 64 ? 2 : 1)
+                               : (QD == 64 || PS == 1 ? 3 : 2);
+  int tiles = 0;
+  for (int j = 0; j < n; ++j) tiles = std::max(tiles, p.job[j].tiles);
+  // jobs of one launch have the same tile count (the caller groups them)
+  const int64_t one = int64_t(tiles) * p.heads * p.batch;
+  if (one > 0x7fffffff / p.nseg) return SSM_ERR_UNSUPPORTED;
+  if (p.nseg > 1) {
+    auto kern = ssm::la::linattn_kernel<T, NP, PS, QD, true, MINB>;
+    constexpr int smem = ssm::la::Layout<T, NP, PS, QD, true>::BYTES;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem) != cudaSuccess) {
+      cudaGetLastError();
+      return SSM_ERR_CUDA;
+    }
+    kern<<<dim3(unsigned(one * (p.nseg - 1)), n), 128, smem, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return SSM_ERR_CUDA;
+    const int64_t el = int64_t(QD) * ssm::kLaTile * one;
+    if (ceil_div(el, 256) > 0x7fffffff) return SSM_ERR_UNSUPPORTED;
+    ssm::la::linattn_join_kernel<QD>
+        <<<dim3(unsigned(ceil_div(el, 256)), n), 256, 0, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return SSM_ERR_CUDA;
+  }
+  auto kern = ssm::la::linattn_kernel<T, NP, PS, QD, false, MINB>;
+  constexpr int smem = ssm::la::Layout<T, NP, PS, QD, false>::BYTES;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           smem) != cudaSuccess) {
+    cudaGetLastError();
+    return SSM_ERR_CUDA;
+  }
+  kern<<<dim3(unsigned(one * p.nseg), n), 128, smem, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
+}
+
+int run_jobs(const LaParams &p, int n, int dtype, bool exact, cudaStream_t s) {
+  const int qd = key_pad(p.job[0].qd);
+  if (dtype == SSM_F32)
+    return qd == 64 ? launch_jobs<float, 3, 3, 64>(p, n, s)
+                    : launch_jobs<float, 3, 3, 128>(p, n, s);
+  if (exact)
+    return qd == 64 ? launch_jobs<bf16, 1, 3, 64>(p, n, s)
+                    : launch_jobs<bf16, 1, 3, 128>(p, n, s);
+  return qd == 64 ? launch_jobs<bf16, 1, 1, 64>(p, n, s)
+                  : launch_jobs<bf16, 1, 1, 128>(p, n, s);
+}
+
+bool check_floats(std::initializer_list<const float *> list) {
+  for (const float *q : list)
+    if (q && !aligned(q, 4)) return false;
+  return true;
+}
+
+LaParams common(const ssm_linattn_dims &d, const Plan &pl,
+                const void *log_decay, const float *head_log_decay,
+                const int *lengths) {
+  LaParams p{};
+  p.log_decay = log_decay;
+  p.head_log_decay = head_log_decay;
+  p.lengths = lengths;
+  p.batch = d.batch;
+  p.seqlen = d.seqlen;
+  p.heads = int(d.heads);
+  p.nseg = pl.nseg;
+  p.seg_len = pl.seg_len;
+  return p;
+}
+
+template <typename T>
+void group_sum(const float *part, const ssm_linattn_dims &d, void *out,
+               cudaStream_t s) {
+  const int64_t n = d.batch * d.seqlen * d.groups * d.dk;
+  const int64_t grid = std::min<int64_t>(ceil_div(n, 256), 148 * 16);
+  ssm::la::linattn_group_sum_kernel<T><<<unsigned(grid), 256, 0, s>>>(
+      part, d.batch * d.seqlen, int(d.groups), int(d.heads / d.groups),
+      int(d.dk), static_cast<T *>(out));
+}
+
+}  // namespace
+
+extern "C" {
+
+int ssm_linattn_workspace(int device, ssm_linattn_dims dims, int dtype,
+                          int backward, size_t *bytes) {
+  if (!bytes) return SSM_ERR_INVALID;
+  *bytes = 0;
+  int rc = check_dims(&dims, dtype,
+                      backward ? ssm::kLaMaxKey : SSM_LINATTN_MAX_VALUE);
+  if (rc != SSM_OK) return rc;
+  int sms = 0;
+  rc = ssm::device_sms(device, &sms);
+  if (rc != SSM_OK) return rc;
+  *bytes = backward ? std::max(plan_bwd(dims, dtype, true, sms).bytes,
+                               plan_bwd(dims, dtype, false, sms).bytes)
+                    : plan_fwd(dims, dtype, sms).bytes;
+  return SSM_OK;
+}
+
+int ssm_linattn_fwd(int device, const void *q, const void *k, const void *v,
+                    const void *log_decay, const float *head_log_decay,
+                    float scale, const int32_t *lengths, const float *h0,
+                    void *y, float *h_last, void *workspace,
+                    size_t workspace_bytes, ssm_linattn_dims dims, int dtype,
+                    struct CUstream_st *stream) {
+  // ---- host-side validation: nothing touches the GPU before it passes
+  if (!q || !k || !v || !y) return SSM_ERR_INVALID;
+  int rc = check_dims(&dims, dtype, SSM_LINATTN_MAX_VALUE);
+  if (rc != SSM_OK) return rc;
+  const size_t esz = dtype == SSM_F32 ? 4 : 2;
+  for (const void *a : {q, k, v, log_decay, static_cast<const void *>(y)})
+    if (a && !aligned(a, esz)) return SSM_ERR_ALIGN;
+  // y is written in pairs of values
+  if (dims.dv % 2 == 0 && !aligned(y, 2 * esz)) return SSM_ERR_ALIGN;
+  if (!check_floats({head_log_decay, h0, h_last,
+                     reinterpret_cast<const float *>(lengths)}))
+    return SSM_ERR_ALIGN;
+  int sms = 0;
+  rc = ssm::device_ready(device, &sms);
+  if (rc != SSM_OK) return rc;
+  const Plan pl = plan_fwd(dims, dtype, sms);
+  if (pl.bytes > workspace_bytes || (pl.bytes && !workspace))
+    return SSM_ERR_INVALID;
+  if (workspace && !aligned(workspace, 16)) return SSM_ERR_ALIGN;
+  unsigned char *ws = static_cast<unsigned char *>(workspace);
+
+  LaParams p = common(dims, pl, log_decay, head_log_decay, lengths);
+  LaJob &j = p.job[0];
+  j.q = q; j.k = k; j.v = v; j.y = y;
+  j.q_stride = dims.q_stride; j.k_stride = dims.k_stride;
+  j.v_stride = dims.v_stride;
+  j.q_heads = j.k_heads = int(dims.groups);
+  j.v_heads = int(dims.heads);
+  j.qd = int(dims.dk); j.vd = int(dims.dv);
+  j.tiles = int(ceil_div(dims.dv, ssm::kLaTile));
+  j.init = h0; j.last = h_last;
+  j.state_rs = j.vd; j.state_cs = 1;
+  j.sp = j.si = scale; j.sw = 1.0f;
+  if (pl.nseg > 1) {
+    j.seg_state = reinterpret_cast<float *>(ws + pl.state[0]);
+    j.seg_decay = reinterpret_cast<float *>(ws + pl.decay[0]);
+  }
+  return run_jobs(p, 1, dtype, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int ssm_linattn_step(int device, const void *q, const void *k, const void *v,
+                     const void *log_decay, const float *head_log_decay,
+                     float scale, float *state, void *y, ssm_linattn_dims dims,
+                     int dtype, struct CUstream_st *stream) {
+  if (!q || !k || !v || !state || !y) return SSM_ERR_INVALID;
+  if (dims.seqlen != 1) return SSM_ERR_INVALID;
+  int rc = check_dims(&dims, dtype, SSM_LINATTN_MAX_VALUE);
+  if (rc != SSM_OK) return rc;
+  const size_t esz = dtype == SSM_F32 ? 4 : 2;
+  for (const void *a : {q, k, v, log_decay, static_cast<const void *>(y)})
+    if (a && !aligned(a, esz)) return SSM_ERR_ALIGN;
+  if (!check_floats({head_log_decay, state})) return SSM_ERR_ALIGN;
+  int sms = 0;
+  rc = ssm::device_ready(device, &sms);
+  if (rc != SSM_OK) return rc;
+  LaStepParams p{};
+  p.q = q; p.k = k; p.v = v;
+  p.q_stride = dims.q_stride; p.k_stride = dims.k_stride;
+  p.v_stride = dims.v_stride;
+  p.log_decay = log_decay; p.head_log_decay = head_log_decay;
+  p.scale = scale; p.state = state; p.y = y;
+  p.batch = dims.batch; p.heads = int(dims.heads);
+  p.groups = int(dims.groups); p.dk = int(dims.dk); p.dv = int(dims.dv);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool wide = p.dv % 4 == 0 && aligned(state, 16);
+  const int64_t grid =
+      p.batch * p.heads * ceil_div(p.dv, wide ? 128 : 32);
+  if (grid > 0x7fffffff) return SSM_ERR_UNSUPPORTED;
+  auto kern =
+      dtype == SSM_F32
+          ? (wide ? ssm::la::linattn_step_kernel<float, 4>
+                  : ssm::la::linattn_step_kernel<float, 1>)
+          : (wide ? ssm::la::linattn_step_kernel<bf16, 4>
+                  : ssm::la::linattn_step_kernel<bf16, 1>);
+  kern<<<unsigned(grid), 256, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
+}
+
+int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
+                    const void *log_decay, const float *head_log_decay,
+                    float scale, const int32_t *lengths, const float *h0,
+                    const void *dy, const float *dh_last, void *dq, void *dk,
+                    void *dv, void *dlog_decay, float *dhead_log_decay,
+                    float *dh0, void *workspace, size_t workspace_bytes,
+                    ssm_linattn_dims dims, int dtype,
+                    struct CUstream_st *stream) {
+  // ---- host-side validation: nothing touches the GPU before it passes
+  if (!q || !k || !v || !dy || !dq || !dk || !dv) return SSM_ERR_INVALID;
+  if ((dlog_decay && !log_decay) || (dhead_log_decay && !head_log_decay))
+    return SSM_ERR_INVALID;
+  int rc = check_dims(&dims, dtype, ssm::kLaMaxKey);
+  if (rc != SSM_OK) return rc;
+  const size_t esz = dtype == SSM_F32 ? 4 : 2;
+  for (const void *a : {q, k, v, log_decay, dy, static_cast<const void *>(dq),
+                        static_cast<const void *>(dk),
+                        static_cast<const void *>(dv),
+                        static_cast<const void *>(dlog_decay)})
+    if (a && !aligned(a, esz)) return SSM_ERR_ALIGN;
+  // gradients are written in pairs of values
+  if (dims.dk % 2 == 0 && (!aligned(dq, 2 * esz) || !aligned(dk, 2 * esz)))
+    return SSM_ERR_ALIGN;
+  if (dims.dv % 2 == 0 && !aligned(dv, 2 * esz)) return SSM_ERR_ALIGN;
+  if (!check_floats({head_log_decay, h0, dh_last, dhead_log_decay, dh0,
+                     reinterpret_cast<const float *>(lengths)}))
+    return SSM_ERR_ALIGN;
+  int sms = 0;
+  rc = ssm::device_ready(device, &sms);
+  if (rc != SSM_OK) return rc;
+  const bool gate = dlog_decay || dhead_log_decay;
+  const Plan pl = plan_bwd(dims, dtype, gate, sms);
+  if (pl.bytes > workspace_bytes || (pl.bytes && !workspace))
+    return SSM_ERR_INVALID;
+  if (workspace && !aligned(workspace, 16)) return SSM_ERR_ALIGN;
+  unsigned char *ws = static_cast<unsigned char *>(workspace);
+  auto at = [&](size_t off) { return reinterpret_cast<float *>(ws + off); };
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+
+  const int H = int(dims.heads), G = int(dims.groups), K = int(dims.dk),
+            V = int(dims.dv);
+  const bool shared = G != H;
+  const int64_t dy_stride = int64_t(H) * V;
+  LaJob jq{}, jk{}, jv{};
+  // dq: query dy, key v, value k
+  jq.q = dy; jq.q_stride = dy_stride; jq.q_heads = H;
+  jq.k = v; jq.k_stride = dims.v_stride; jq.k_heads = H;
+  jq.v = k; jq.v_stride = dims.k_stride; jq.v_heads = G;
+  jq.qd = V; jq.vd = K;
+  jq.y = shared ? static_cast<void *>(at(pl.part_dq)) : dq;
+  jq.init = h0; jq.state_rs = 1; jq.state_cs = V;
+  jq.sp = jq.si = scale; jq.sw = 1.0f;
+  // dk: query v, key dy, value q, backwards
+  jk.q = v; jk.q_stride = dims.v_stride; jk.q_heads = H;
+  jk.k = dy; jk.k_stride = dy_stride; jk.k_heads = H;
+  jk.v = q; jk.v_stride = dims.q_stride; jk.v_heads = G;
+  jk.qd = V; jk.vd = K;
+  jk.y = shared ? static_cast<void *>(at(pl.part_dk)) : dk;
+  jk.init = dh_last; jk.state_rs = 1; jk.state_cs = V;
+  jk.sp = jk.sw = scale; jk.si = 1.0f;
+  jk.reverse = 1;
+  jq.y_f32 = jk.y_f32 = shared;
+  jq.tiles = jk.tiles = int(ceil_div(K, ssm::kLaTile));
+  // dv: query k, key q, value dy, backwards
+  jv.q = k; jv.q_stride = dims.k_stride; jv.q_heads = G;
+  jv.k = q; jv.k_stride = dims.q_stride; jv.k_heads = G;
+  jv.v = dy; jv.v_stride = dy_stride; jv.v_heads = H;
+  jv.qd = K; jv.vd = V;
+  jv.y = dv;
+  jv.init = dh_last; jv.last = dh0; jv.state_rs = V; jv.state_cs = 1;
+  jv.sp = jv.sw = scale; jv.si = 1.0f;
+  jv.reverse = 1;
+  jv.tiles = int(ceil_div(V, ssm::kLaTile));
+  if (pl.nseg > 1) {
+    LaJob *all[3] = {&jq, &jk, &jv};
+    for (int i = 0; i < 3; ++i) {
+      all[i]->seg_state = at(pl.state[i]);
+      all[i]->seg_decay = at(pl.decay[i]);
+    }
+  }
+  if (gate) {
+    jq.dot = q; jq.dot_stride = dims.q_stride; jq.dot_heads = G;
+    jk.dot = k; jk.dot_stride = dims.k_stride; jk.dot_heads = G;
+    jq.rows = at(pl.rows_q);
+    jk.rows = at(pl.rows_k);
+    if (dh_last) jq.last = at(pl.last);  // [dk, dv] through the strides
+  }
+
+  LaParams p = common(dims, pl, log_decay, head_log_decay, lengths);
+  p.job[0] = jq;
+  p.job[1] = jk;
+  rc = run_jobs(p, 2, dtype, gate, s);
+  if (rc != SSM_OK) return rc;
+  p.job[0] = jv;
+  rc = run_jobs(p, 1, dtype, false, s);
+  if (rc != SSM_OK) return rc;
+
+  if (shared) {
+    if (dtype == SSM_F32) {
+      group_sum<float>(at(pl.part_dq), dims, dq, s);
+      group_sum<float>(at(pl.part_dk), dims, dk, s);
+    } else {
+      group_sum<bf16>(at(pl.part_dq), dims, dq, s);
+      group_sum<bf16>(at(pl.part_dk), dims, dk, s);
+    }
+    if (cudaGetLastError() != cudaSuccess) return SSM_ERR_CUDA;
+  }
+  if (gate) {
+    LaGateParams g{};
+    g.rows_q = at(pl.rows_q);
+    g.rows_k = at(pl.rows_k);
+    g.tiles = jq.tiles;
+    if (pl.nseg > 1) {
+      g.fwd_state = at(pl.state[0]);
+      g.rev_state = at(pl.state[1]);
+    }
+    g.state_floats = int64_t(jq.tiles) * key_pad(V) * ssm::kLaTile;
+    g.last_state = at(pl.last);
+    g.dh_last = dh_last;
+    g.last_floats = int64_t(K) * V;
+    g.dlog_decay = dlog_decay;
+    g.part = dhead_log_decay ? at(pl.part_head) : nullptr;
+    g.log_decay = log_decay;
+    g.head_log_decay = head_log_decay;
+    g.lengths = lengths;
+    g.batch = dims.batch; g.seqlen = dims.seqlen; g.heads = H;
+    g.nseg = pl.nseg; g.seg_len = pl.seg_len;
+    const int64_t grid = dims.batch * H * pl.nseg;
+    if (grid > 0x7fffffff) return SSM_ERR_UNSUPPORTED;
+    if (dtype == SSM_F32)
+      ssm::la::linattn_gate_kernel<float><<<unsigned(grid), 256, 0, s>>>(g);
+    else
+      ssm::la::linattn_gate_kernel<bf16><<<unsigned(grid), 256, 0, s>>>(g);
+    if (dhead_log_decay)
+      ssm::la::linattn_head_sum_kernel<<<H, 128, 0, s>>>(
+          g.part, dims.batch * pl.nseg, H, dhead_log_decay);
+    if (cudaGetLastError() != cudaSuccess) return SSM_ERR_CUDA;
+  }
+  return SSM_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,124 @@
+"""Layer norm with the residual sum in front (include/ssm_layernorm.h)."""
+from __future__ import annotations
+
+import ctypes
+
+from . import _check, _ptr, _stream, library
+from ._launch import dense, dtype_code, launching
+
+
+def ssm_layernorm_workspace(device, rows, dim, dtype) -> int:
+    """Bytes of workspace the backward call needs for its weight gradients."""
+    n = ctypes.c_size_t(0)
+    _check(library().ssm_layernorm_workspace(int(device), int(rows), int(dim),
+                                             int(dtype), ctypes.byref(n)),
+           "ssm_layernorm_workspace")
+    return n.value
+
+
+def ssm_layernorm_fwd(device, x, residual, weight, bias, eps, y, sum, mean,
+                      rstd, rows, dim, dtype, stream=None, check=True) -> int:
+    """Call ssm_layernorm_fwd with tensors (or raw addresses). Returns the
+    status; raises unless ``check`` is False."""
+    rc = library().ssm_layernorm_fwd(
+        int(device), _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), eps,
+        _ptr(y), _ptr(sum), _ptr(mean), _ptr(rstd), int(rows), int(dim),
+        int(dtype), _stream(stream))
+    return _check(rc, "ssm_layernorm_fwd") if check else rc
+
+
+def ssm_layernorm_bwd(device, dy, x, mean, rstd, weight, dsum, dx, dweight,
+                      dbias, workspace, workspace_bytes, rows, dim, dtype,
+                      stream=None, check=True) -> int:
+    """Call ssm_layernorm_bwd (gradients; see include/ssm_layernorm.h)."""
+    rc = library().ssm_layernorm_bwd(
+        int(device), _ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight),
+        _ptr(dsum), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(workspace),
+        int(workspace_bytes), int(rows), int(dim), int(dtype),
+        _stream(stream))
+    return _check(rc, "ssm_layernorm_bwd") if check else rc
+
+
+class LayerNorm:
+    """Layer norm over the last dimension, on one device.
+
+    x, residual: contiguous [..., D], float32 or bfloat16; weight, bias: [D]
+    float32 or None. The object keeps no device memory: calls may run at once
+    on several streams and threads, and be captured into CUDA graphs.
+    """
+
+    def __init__(self, device: int = 0):
+        import torch
+        library()
+        self.device = torch.device("cuda", int(device))
+        self._bytes = {}
+
+    def _rows(self, x):
+        if x.dim() < 1 or x.numel() == 0:
+            raise ValueError("x must have at least one row")
+        return x.numel() // x.shape[-1], x.shape[-1]
+
+    def __call__(self, x, weight=None, bias=None, residual=None, eps=1e-5,
+                 y=None, stream=None):
+        """Norms s = x + residual (rounded to x's type). Returns a dict: y,
+        sum (None without residual), mean and rstd [rows] float32, which the
+        backward pass takes."""
+        import torch
+        code = dtype_code(x)
+        shape = tuple(x.shape)
+        rows, dim = self._rows(x)
+        dense("x", x, shape, x.dtype, self.device)
+        dense("residual", residual, shape, x.dtype, self.device)
+        dense("y", y, shape, x.dtype, self.device)
+        dense("weight", weight, (dim,), torch.float32, self.device)
+        dense("bias", bias, (dim,), torch.float32, self.device)
+        with launching(self.device, stream) as s:
+            if y is None:
+                y = torch.empty_like(x)
+            out = dict(
+                y=y, sum=None if residual is None else torch.empty_like(x),
+                mean=torch.empty(rows, dtype=torch.float32,
+                                 device=self.device),
+                rstd=torch.empty(rows, dtype=torch.float32,
+                                 device=self.device))
+            ssm_layernorm_fwd(self.device.index, x, residual, weight, bias,
+                              eps, y, out["sum"], out["mean"], out["rstd"],
+                              rows, dim, code, s)
+        return out
+
+    def backward(self, dy, x, mean, rstd, weight=None, bias=None, dsum=None,
+                 stream=None):
+        """Gradients of sum(dy * y) + sum(dsum * s). x: what was normed (the
+        forward's sum where there was a residual); mean, rstd: the forward's.
+        Returns a dict: dx (of x, and of the residual), dweight, dbias
+        (float32; None without weight / bias)."""
+        import torch
+        code = dtype_code(x)
+        shape = tuple(x.shape)
+        rows, dim = self._rows(x)
+        f32 = torch.float32
+        if dy is None or mean is None or rstd is None:
+            raise ValueError("dy, mean and rstd are required")
+        for name, t in (("x", x), ("dy", dy), ("dsum", dsum)):
+            dense(name, t, shape, x.dtype, self.device)
+        for name, t in (("mean", mean), ("rstd", rstd)):
+            dense(name, t, (rows,), f32, self.device)
+        dense("weight", weight, (dim,), f32, self.device)
+        dense("bias", bias, (dim,), f32, self.device)
+        with launching(self.device, stream) as s:
+            f = dict(dtype=f32, device=self.device)
+            g = dict(dx=torch.empty_like(x),
+                     dweight=None if weight is None else torch.empty(dim, **f),
+                     dbias=None if bias is None else torch.empty(dim, **f))
+            ws, n = None, 0
+            if weight is not None or bias is not None:
+                key = (rows, dim, code)
+                n = self._bytes.get(key)
+                if n is None:
+                    n = self._bytes[key] = ssm_layernorm_workspace(
+                        self.device.index, rows, dim, code)
+                ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+            ssm_layernorm_bwd(self.device.index, dy, x, mean, rstd, weight,
+                              dsum, g["dx"], g["dweight"], g["dbias"], ws, n,
+                              rows, dim, code, s)
+        return g
