@@ -2,8 +2,6 @@
 device, buffers allocated where the launch will use them."""
 from __future__ import annotations
 
-import contextlib
-
 
 def dtype_code(t):
     import torch
@@ -19,10 +17,15 @@ def dense(name, t, shape, dtype, device):
     """Raise unless t is None or a contiguous tensor of that description."""
     if t is None:
         return
-    if (t.dtype != dtype or t.device != device or tuple(t.shape) != shape
-            or not t.is_contiguous()):
+    if (t.shape != shape or t.dtype != dtype or not t.is_contiguous()
+            or t.device != device):
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
-                         % (name, dtype, shape, device))
+                         % (name, dtype, tuple(shape), device))
+
+
+def ptr(t):
+    """Device address of a tensor, None for None."""
+    return None if t is None else t.data_ptr()
 
 
 def apart(**tensors):
@@ -35,23 +38,23 @@ def apart(**tensors):
             raise ValueError("%s and %s must not overlap" % (a, b))
 
 
-@contextlib.contextmanager
-def launching(device, stream):
-    """The raw stream to launch on, with `device` current and torch's
-    allocations made on that stream (so that a workspace or a result is never
-    handed to, or taken from, work that another stream still has to do)."""
+def launch(device, stream, call, *args):
+    """call(raw stream, *args) with `device` current and torch's allocations
+    made on that stream (so that a workspace or a result is never handed to,
+    or taken from, work that another stream still has to do). stream: None
+    for torch's current stream of the device, a torch stream or a raw one."""
     import torch
     if stream is None:
         if torch.cuda.current_device() == device.index:
-            yield torch.cuda.current_stream(device).cuda_stream
-        else:
-            with torch.cuda.device(device):
-                yield torch.cuda.current_stream(device).cuda_stream
-        return
+            return call(torch._C._cuda_getCurrentRawStream(device.index),
+                        *args)
+        with torch.cuda.device(device):
+            return call(torch._C._cuda_getCurrentRawStream(device.index),
+                        *args)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
     if stream.device != device:
         raise ValueError("stream belongs to %s, not %s" % (stream.device,
                                                            device))
     with torch.cuda.stream(stream):   # also makes its device current
-        yield stream.cuda_stream
+        return call(stream.cuda_stream, *args)

@@ -50,24 +50,32 @@ using bf16 = __nv_bfloat16;
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
 
-// V elements from (streamed: read once) or to global memory.
+// V elements as they lie in memory, in registers.
 template <typename T, int V>
-__device__ __forceinline__ void load(const T *p, float (&f)[V]) {
-  if constexpr (V == 1) {
-    f[0] = to_f(*p);
-  } else if constexpr (sizeof(T) == 4) {
-    const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-  } else {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[2 * j] = __uint_as_float(w[j] << 16);
-      f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+struct Raw {
+  uint32_t w[V == 1 ? 1 : 4];
+
+  // Read once: streamed past the caches' other contents.
+  __device__ __forceinline__ void load(const T *p) {
+    if constexpr (V == 1) {
+      if constexpr (sizeof(T) == 4) w[0] = __float_as_uint(*p);
+      else w[0] = uint32_t(*reinterpret_cast<const uint16_t *>(p)) << 16;
+    } else {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
     }
   }
-}
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < (V == 1 ? 1 : 4); ++j) w[j] = 0u;
+  }
+  __device__ __forceinline__ float at(int j) const {
+    if constexpr (V == 1 || sizeof(T) == 4)
+      return __uint_as_float(w[j]);
+    else
+      return __uint_as_float(j % 2 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+  }
+};
 
 template <typename T, int V>
 __device__ __forceinline__ void store(T *p, const float (&f)[V]) {
@@ -87,7 +95,7 @@ __device__ __forceinline__ void store(T *p, const float (&f)[V]) {
   }
 }
 
-// V parameters (kept in cache: every row reads them).
+// V parameters.
 template <int V>
 __device__ __forceinline__ void load_param(const float *p, float (&f)[V]) {
   if constexpr (V == 1) {
@@ -128,46 +136,68 @@ __device__ __forceinline__ void row_sum2(float &a, float &b, int wpr,
   }
 }
 
+// Blocks stay for many rows: a thread's parameters are read once, and the next
+// row is on its way while this one is reduced and written.
 template <typename T, int V, int N, int G>
 __global__ void __launch_bounds__(512)
     layernorm_fwd_kernel(const __grid_constant__ NormParams p) {
   __shared__ float2 red[64];
   const int lanes = G < 32 ? G : 32 * p.wpr;       // threads of a row
   const int per = blockDim.x / lanes;              // rows of a block
-  const int lane = threadIdx.x % lanes;
+  const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes;
   const float inv = 1.0f / float(p.dim);
   const int64_t steps = (p.rows + per - 1) / per;
+  float w[N][V], b[N][V];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int c = (i * lanes + lane) * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      w[i][j] = 1.0f;
+      b[i][j] = 0.0f;
+    }
+    if (c < p.dim && p.weight) load_param<V>(p.weight + c, w[i]);
+    if (c < p.dim && p.bias) load_param<V>(p.bias + c, b[i]);
+  }
+  Raw<T, V> nx[N], nr[N];
+  auto fetch = [&](int64_t st) {
+    const int64_t row = st * per + group;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * lanes + lane) * V;
+      nx[i].zero();
+      nr[i].zero();
+      if (row < p.rows && c < p.dim) {
+        nx[i].load(static_cast<const T *>(p.x) + row * p.dim + c);
+        if (p.residual)
+          nr[i].load(static_cast<const T *>(p.residual) + row * p.dim + c);
+      }
+    }
+  };
+  fetch(blockIdx.x);
   for (int64_t st = blockIdx.x; st < steps; st += gridDim.x) {
-    const int64_t row = st * per + threadIdx.x / lanes;
+    const int64_t row = st * per + group;
     const bool in = row < p.rows;
     const int64_t base = row * p.dim;
     float f[N][V];
     float s = 0.0f, none = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = (i * lanes + lane) * V;
+    for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int j = 0; j < V; ++j) f[i][j] = 0.0f;
-      if (in && c < p.dim)
-        load<T, V>(static_cast<const T *>(p.x) + base + c, f[i]);
-    }
-    if (p.residual) {
+      for (int j = 0; j < V; ++j) {
+        f[i][j] = nx[i].at(j);
+        if (p.residual) f[i][j] = to_f(T(f[i][j] + nr[i].at(j)));
+        s += f[i][j];
+      }
+    fetch(st + gridDim.x);
+    if (p.sum) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int c = (i * lanes + lane) * V;
-        if (in && c < p.dim) {
-          float r[V];
-          load<T, V>(static_cast<const T *>(p.residual) + base + c, r);
-#pragma unroll
-          for (int j = 0; j < V; ++j) f[i][j] = to_f(T(f[i][j] + r[j]));
-          if (p.sum) store<T, V>(static_cast<T *>(p.sum) + base + c, f[i]);
-        }
+        if (in && c < p.dim)
+          store<T, V>(static_cast<T *>(p.sum) + base + c, f[i]);
       }
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-      for (int j = 0; j < V; ++j) s += f[i][j];
     row_sum2<G>(s, none, p.wpr, red, 0);
     const float mean = s * inv;
     float q = 0.0f;
@@ -177,8 +207,8 @@ __global__ void __launch_bounds__(512)
       if (c < p.dim) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float d = f[i][j] - mean;
-          q = fmaf(d, d, q);
+          f[i][j] -= mean;
+          q = fmaf(f[i][j], f[i][j], q);
         }
       }
     }
@@ -193,19 +223,8 @@ __global__ void __launch_bounds__(512)
       const int c = (i * lanes + lane) * V;
       if (in && c < p.dim) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) f[i][j] = (f[i][j] - mean) * rstd;
-        if (p.weight) {
-          float w[V];
-          load_param<V>(p.weight + c, w);
-#pragma unroll
-          for (int j = 0; j < V; ++j) f[i][j] *= w[j];
-        }
-        if (p.bias) {
-          float w[V];
-          load_param<V>(p.bias + c, w);
-#pragma unroll
-          for (int j = 0; j < V; ++j) f[i][j] += w[j];
-        }
+        for (int j = 0; j < V; ++j)
+          f[i][j] = fmaf(f[i][j] * rstd, w[i][j], b[i][j]);
         store<T, V>(static_cast<T *>(p.y) + base + c, f[i]);
       }
     }
@@ -234,46 +253,61 @@ __global__ void __launch_bounds__(512)
 #pragma unroll
     for (int j = 0; j < V; ++j)
       dw[i][j] = db[i][j] = dw2[i][j] = db2[i][j] = 0.0f;
+  float w[N][V];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int c = (i * lanes + lane) * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j) w[i][j] = 1.0f;
+    if (c < p.dim && p.weight) load_param<V>(p.weight + c, w[i]);
+  }
+  Raw<T, V> nx[N], ng[N], nd[N];
+  float nmean = 0.0f, nrstd = 0.0f;
+  auto fetch = [&](int64_t st) {
+    const int64_t row = st * per + group;
+    const bool in = row < p.rows;
+    nmean = in ? p.mean[row] : 0.0f;
+    nrstd = in ? p.rstd[row] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * lanes + lane) * V;
+      nx[i].zero();
+      ng[i].zero();
+      nd[i].zero();
+      if (in && c < p.dim) {
+        const int64_t at = row * p.dim + c;
+        nx[i].load(static_cast<const T *>(p.x) + at);
+        ng[i].load(static_cast<const T *>(p.dy) + at);
+        if (p.dsum) nd[i].load(static_cast<const T *>(p.dsum) + at);
+      }
+    }
+  };
+  fetch(blockIdx.x);
   int fold = 0, slot = 0;
   for (int64_t st = blockIdx.x; st < steps; st += gridDim.x, slot ^= 1) {
     const int64_t row = st * per + group;
     const bool in = row < p.rows;
     const int64_t base = row * p.dim;
-    float x[N][V], g[N][V];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = (i * lanes + lane) * V;
-#pragma unroll
-      for (int j = 0; j < V; ++j) x[i][j] = g[i][j] = 0.0f;
-      if (in && c < p.dim) {
-        load<T, V>(static_cast<const T *>(p.x) + base + c, x[i]);
-        load<T, V>(static_cast<const T *>(p.dy) + base + c, g[i]);
-      }
-    }
-    const float mean = in ? p.mean[row] : 0.0f;
-    const float rstd = in ? p.rstd[row] : 0.0f;
+    const float mean = nmean, rstd = nrstd;
+    float x[N][V], g[N][V], ds[N][V];
     float su = 0.0f, sux = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = (i * lanes + lane) * V;
-      if (c < p.dim) {
-        float w[V];
+      const bool live = c < p.dim;
 #pragma unroll
-        for (int j = 0; j < V; ++j) w[j] = 1.0f;
-        if (p.weight) load_param<V>(p.weight + c, w);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          x[i][j] = (x[i][j] - mean) * rstd;
-          if (p.part) {
-            dw[i][j] = fmaf(g[i][j], x[i][j], dw[i][j]);
-            db[i][j] += g[i][j];
-          }
-          g[i][j] *= w[j];
-          su += g[i][j];
-          sux = fmaf(g[i][j], x[i][j], sux);
-        }
+      for (int j = 0; j < V; ++j) {
+        x[i][j] = live ? (nx[i].at(j) - mean) * rstd : 0.0f;
+        g[i][j] = ng[i].at(j);
+        ds[i][j] = nd[i].at(j);
+        dw[i][j] = fmaf(g[i][j], x[i][j], dw[i][j]);
+        db[i][j] += g[i][j];
+        g[i][j] *= w[i][j];
+        su += g[i][j];
+        sux = fmaf(g[i][j], x[i][j], sux);
       }
     }
+    fetch(st + gridDim.x);
     row_sum2<G>(su, sux, p.wpr, red, slot);
     su *= inv;
     sux *= inv;
@@ -284,13 +318,7 @@ __global__ void __launch_bounds__(512)
         float o[V];
 #pragma unroll
         for (int j = 0; j < V; ++j)
-          o[j] = (g[i][j] - su - x[i][j] * sux) * rstd;
-        if (p.dsum) {
-          float r[V];
-          load<T, V>(static_cast<const T *>(p.dsum) + base + c, r);
-#pragma unroll
-          for (int j = 0; j < V; ++j) o[j] += r[j];
-        }
+          o[j] = fmaf(g[i][j] - su - x[i][j] * sux, rstd, ds[i][j]);
         store<T, V>(static_cast<T *>(p.dx) + base + c, o);
       }
     }

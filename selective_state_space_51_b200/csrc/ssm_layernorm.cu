@@ -23,13 +23,16 @@ struct Shape {
   int threads = 256, per = 1;  // of a block; rows of a block
 };
 
-// `most`: groups of V elements a thread may hold.
-Shape shape_of(int dim, int v, int most) {
+// A thread holds at most 2 groups of 16 bytes, or 4 single elements: more of
+// them cost residency (registers) than they save barriers. Rows wider than 16
+// warps' worth of that (the launch bound) take more.
+Shape shape_of(int dim, int v) {
   Shape s;
   const int nv = int(ceil_div(dim, v));
   if (nv <= 16) {
     s.g = nv <= 4 ? 4 : nv <= 8 ? 8 : 16;
   } else {
+    const int most = std::max<int>(v == 1 ? 4 : 2, int(ceil_div(nv, 512)));
     s.wpr = int(ceil_div(nv, 32 * most));
     s.n = int(ceil_div(nv, 32 * s.wpr));
   }
@@ -46,16 +49,26 @@ int parts_of(const Shape &s, int64_t rows, int sms) {
   return int(std::min<int64_t>(ceil_div(rows, s.per), int64_t(sms) * per_sm));
 }
 
-// Groups a thread may hold: 16 elements (32 in the forward pass with
-// bfloat16). The widest row then takes 16 warps, the launch bound.
-int most_groups(int v, bool bwd) { return v == 8 && !bwd ? 4 : 16 / v; }
+// Blocks of `threads` that an SM holds at once.
+int resident(const void *kern, int threads) {
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0) !=
+          cudaSuccess ||
+      n < 1) {
+    cudaGetLastError();
+    n = 1;
+  }
+  return n;
+}
 
 template <typename T, int V, int N, int G>
 int launch_fwd(const NormParams &p, const Shape &s, int sms, cudaStream_t st) {
   const int64_t steps = ceil_div(p.rows, s.per);
-  const int64_t grid = std::min<int64_t>(steps, int64_t(sms) * 64);
-  ssm::norm::layernorm_fwd_kernel<T, V, N, G>
-      <<<unsigned(grid), s.threads, 0, st>>>(p);
+  auto kern = ssm::norm::layernorm_fwd_kernel<T, V, N, G>;
+  const int64_t grid = std::min<int64_t>(
+      steps, int64_t(sms) * resident(reinterpret_cast<const void *>(kern),
+                                     s.threads));
+  kern<<<unsigned(grid), s.threads, 0, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
 
@@ -91,7 +104,7 @@ int pick(const NormParams &p, const Shape &s, int sms, cudaStream_t st) {
   if (s.g == 16) return launch<T, V, BWD, 1, 16>(p, s, sms, st);
   if (s.n == 1) return launch<T, V, BWD, 1, 32>(p, s, sms, st);
   if (s.n == 2) return launch<T, V, BWD, 2, 32>(p, s, sms, st);
-  if constexpr (V < 8 || !BWD) {
+  if constexpr (V < 8) {
     if (s.n <= 3) return launch<T, V, BWD, 3, 32>(p, s, sms, st);
     if (s.n <= 4) return launch<T, V, BWD, 4, 32>(p, s, sms, st);
   }
@@ -138,10 +151,8 @@ bool wide_rows(int64_t dim, size_t esz,
 
 int width(bool wide, size_t esz) { return wide ? int(16 / esz) : 1; }
 
-// The backward pass's layout: the widest of what alignment may leave it.
-Shape bwd_shape(int64_t dim, bool wide, size_t esz) {
-  const int v = width(wide, esz);
-  return shape_of(int(dim), v, most_groups(v, true));
+Shape row_shape(int64_t dim, bool wide, size_t esz) {
+  return shape_of(int(dim), width(wide, esz));
 }
 
 }  // namespace
@@ -158,9 +169,9 @@ int ssm_layernorm_workspace(int device, int64_t rows, int64_t dim, int dtype,
   rc = ssm::device_sms(device, &sms);
   if (rc != SSM_OK) return rc;
   const size_t esz = dtype == SSM_F32 ? 4 : 2;
-  int parts = parts_of(bwd_shape(dim, false, esz), rows, sms);
+  int parts = parts_of(row_shape(dim, false, esz), rows, sms);
   if (dim * esz % 16 == 0)
-    parts = std::max(parts, parts_of(bwd_shape(dim, true, esz), rows, sms));
+    parts = std::max(parts, parts_of(row_shape(dim, true, esz), rows, sms));
   *bytes = size_t(parts) * 2 * dim * sizeof(float);
   return SSM_OK;
 }
@@ -188,8 +199,7 @@ int ssm_layernorm_fwd(int device, const void *x, const void *residual,
   p.y = y; p.sum = sum; p.mean = mean; p.rstd = rstd; p.eps = eps;
   p.rows = rows; p.dim = int(dim);
   const bool wide = wide_rows(dim, esz, {x, residual, y, sum, weight, bias});
-  const int v = width(wide, esz);
-  const Shape s = shape_of(p.dim, v, most_groups(v, false));
+  const Shape s = row_shape(dim, wide, esz);
   p.wpr = s.wpr;
   return run(p, wide, false, dtype, s, sms,
              reinterpret_cast<cudaStream_t>(stream));
@@ -220,7 +230,7 @@ int ssm_layernorm_bwd(int device, const void *dy, const void *x,
   p.dweight = dweight; p.dbias = dbias;
   p.rows = rows; p.dim = int(dim);
   const bool wide = wide_rows(dim, esz, {dy, x, dsum, dx, weight});
-  const Shape s = bwd_shape(dim, wide, esz);
+  const Shape s = row_shape(dim, wide, esz);
   p.wpr = s.wpr;
   p.parts = parts_of(s, rows, sms);
   if (dweight || dbias) {

@@ -4,7 +4,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _check, _ptr, _stream, library
-from ._launch import dense, dtype_code, launching
+from ._launch import dense, dtype_code, launch, ptr
 
 
 def ssm_layernorm_workspace(device, rows, dim, dtype) -> int:
@@ -49,7 +49,7 @@ class LayerNorm:
 
     def __init__(self, device: int = 0):
         import torch
-        library()
+        self._lib = library()
         self.device = torch.device("cuda", int(device))
         self._bytes = {}
 
@@ -65,26 +65,27 @@ class LayerNorm:
         backward pass takes."""
         import torch
         code = dtype_code(x)
-        shape = tuple(x.shape)
         rows, dim = self._rows(x)
-        dense("x", x, shape, x.dtype, self.device)
-        dense("residual", residual, shape, x.dtype, self.device)
-        dense("y", y, shape, x.dtype, self.device)
+        dense("x", x, x.shape, x.dtype, self.device)
+        dense("residual", residual, x.shape, x.dtype, self.device)
+        dense("y", y, x.shape, x.dtype, self.device)
         dense("weight", weight, (dim,), torch.float32, self.device)
         dense("bias", bias, (dim,), torch.float32, self.device)
-        with launching(self.device, stream) as s:
-            if y is None:
-                y = torch.empty_like(x)
-            out = dict(
-                y=y, sum=None if residual is None else torch.empty_like(x),
-                mean=torch.empty(rows, dtype=torch.float32,
-                                 device=self.device),
-                rstd=torch.empty(rows, dtype=torch.float32,
-                                 device=self.device))
-            ssm_layernorm_fwd(self.device.index, x, residual, weight, bias,
-                              eps, y, out["sum"], out["mean"], out["rstd"],
-                              rows, dim, code, s)
-        return out
+        return launch(self.device, stream, self._forward, x, weight, bias,
+                      residual, eps, y, rows, dim, code)
+
+    def _forward(self, s, x, weight, bias, residual, eps, y, rows, dim, code):
+        import torch
+        if y is None:
+            y = torch.empty_like(x)
+        total = None if residual is None else torch.empty_like(x)
+        mean = torch.empty(rows, dtype=torch.float32, device=self.device)
+        rstd = torch.empty(rows, dtype=torch.float32, device=self.device)
+        _check(self._lib.ssm_layernorm_fwd(
+            self.device.index, x.data_ptr(), ptr(residual), ptr(weight),
+            ptr(bias), eps, y.data_ptr(), ptr(total), mean.data_ptr(),
+            rstd.data_ptr(), rows, dim, code, s), "ssm_layernorm_fwd")
+        return dict(y=y, sum=total, mean=mean, rstd=rstd)
 
     def backward(self, dy, x, mean, rstd, weight=None, bias=None, dsum=None,
                  stream=None):
@@ -94,31 +95,38 @@ class LayerNorm:
         (float32; None without weight / bias)."""
         import torch
         code = dtype_code(x)
-        shape = tuple(x.shape)
         rows, dim = self._rows(x)
-        f32 = torch.float32
         if dy is None or mean is None or rstd is None:
             raise ValueError("dy, mean and rstd are required")
-        for name, t in (("x", x), ("dy", dy), ("dsum", dsum)):
-            dense(name, t, shape, x.dtype, self.device)
-        for name, t in (("mean", mean), ("rstd", rstd)):
-            dense(name, t, (rows,), f32, self.device)
+        f32 = torch.float32
+        dense("x", x, x.shape, x.dtype, self.device)
+        dense("dy", dy, x.shape, x.dtype, self.device)
+        dense("dsum", dsum, x.shape, x.dtype, self.device)
+        dense("mean", mean, (rows,), f32, self.device)
+        dense("rstd", rstd, (rows,), f32, self.device)
         dense("weight", weight, (dim,), f32, self.device)
         dense("bias", bias, (dim,), f32, self.device)
-        with launching(self.device, stream) as s:
-            f = dict(dtype=f32, device=self.device)
-            g = dict(dx=torch.empty_like(x),
-                     dweight=None if weight is None else torch.empty(dim, **f),
-                     dbias=None if bias is None else torch.empty(dim, **f))
-            ws, n = None, 0
-            if weight is not None or bias is not None:
-                key = (rows, dim, code)
-                n = self._bytes.get(key)
-                if n is None:
-                    n = self._bytes[key] = ssm_layernorm_workspace(
-                        self.device.index, rows, dim, code)
-                ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-            ssm_layernorm_bwd(self.device.index, dy, x, mean, rstd, weight,
-                              dsum, g["dx"], g["dweight"], g["dbias"], ws, n,
-                              rows, dim, code, s)
-        return g
+        return launch(self.device, stream, self._backward, dy, x, mean, rstd,
+                      weight, bias, dsum, rows, dim, code)
+
+    def _backward(self, s, dy, x, mean, rstd, weight, bias, dsum, rows, dim,
+                  code):
+        import torch
+        f = dict(dtype=torch.float32, device=self.device)
+        dx = torch.empty_like(x)
+        dweight = None if weight is None else torch.empty(dim, **f)
+        dbias = None if bias is None else torch.empty(dim, **f)
+        ws, n = None, 0
+        if weight is not None or bias is not None:
+            key = (rows, dim, code)
+            n = self._bytes.get(key)
+            if n is None:
+                n = self._bytes[key] = ssm_layernorm_workspace(
+                    self.device.index, rows, dim, code)
+            ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        _check(self._lib.ssm_layernorm_bwd(
+            self.device.index, dy.data_ptr(), x.data_ptr(), mean.data_ptr(),
+            rstd.data_ptr(), ptr(weight), ptr(dsum), dx.data_ptr(),
+            ptr(dweight), ptr(dbias), ptr(ws), n, rows, dim, code, s),
+            "ssm_layernorm_bwd")
+        return dict(dx=dx, dweight=dweight, dbias=dbias)

@@ -4,7 +4,7 @@ from __future__ import annotations
 import ctypes
 
 from . import (_check, _ptr, _stream, library, ssm_linattn_dims)
-from ._launch import apart, dense, dtype_code, launching
+from ._launch import apart, dense, dtype_code, launch, ptr
 
 
 def _dims(dims):
@@ -77,44 +77,55 @@ class LinearAttention:
 
     def __init__(self, device: int = 0):
         import torch
-        library()
+        self._lib = library()
         self.device = torch.device("cuda", int(device))
         self._bytes = {}
 
-    def _rows(self, name, t, b, L, heads, d, dtype):
-        """Elements from one token of `t` to the next."""
-        s = t.stride() if t.dim() == 4 else None
-        if (s is None or tuple(t.shape) != (b, L, heads, d)
-                or t.dtype != dtype or t.device != self.device):
+    def _rows(self, name, t, shape, dtype):
+        """Elements from one token of `t` to the next; shape: (b, L, heads,
+        size), or (b, heads, size) for one token."""
+        if t.shape != shape or t.dtype != dtype or t.device != self.device:
             raise ValueError("%s must be a %s tensor of shape %s on %s" % (
-                name, dtype, (b, L, heads, d), self.device))
-        step = s[1] if L > 1 else s[0] if b > 1 else heads * d
-        if ((d > 1 and s[3] != 1) or (heads > 1 and s[2] != d)
-                or step < heads * d or (L > 1 and b > 1 and s[0] != L * step)):
+                name, dtype, tuple(shape), self.device))
+        s = t.stride()
+        heads, d = shape[-2:]
+        if len(shape) == 4 and shape[1] > 1:
+            step = s[1]
+            even = shape[0] == 1 or s[0] == shape[1] * step
+        else:
+            step, even = (s[0] if shape[0] > 1 else heads * d), True
+        if not (even and step >= heads * d and (d == 1 or s[-1] == 1)
+                and (heads == 1 or s[-2] == d)):
             raise ValueError(
                 "%s must hold each token's heads in one piece, with one "
                 "distance between all tokens" % name)
         return step
 
-    def _inputs(self, q, k, v, log_decay, head_log_decay, lengths, scale):
+    def _inputs(self, q, k, v, log_decay, head_log_decay, lengths, scale,
+                rank=4):
         import torch
-        if q.dim() != 4 or v.dim() != 4:
-            raise ValueError("q, k and v must have the dimensions "
-                             "[batch, tokens, heads, size]")
-        code = dtype_code(q)
-        b, L, G, dk = q.shape
-        H, dv = v.shape[2:]
-        if G == 0 or H % G:
-            raise ValueError("v's heads must be a multiple of q's")
-        dims = (b, L, H, G, dk, dv,
-                self._rows("q", q, b, L, G, dk, q.dtype),
-                self._rows("k", k, b, L, G, dk, q.dtype),
-                self._rows("v", v, b, L, H, dv, q.dtype))
-        dense("log_decay", log_decay, (b, L, H), q.dtype, self.device)
-        dense("head_log_decay", head_log_decay, (H,), torch.float32,
-              self.device)
-        dense("lengths", lengths, (b,), torch.int32, self.device)
-        return dims, code, dk ** -0.5 if scale is None else float(scale)
+        if q.dim() != rank or v.dim() != rank:
+            raise ValueError("q, k and v must have the dimensions [batch, "
+                             "%sheads, size]" % ("tokens, " if rank == 4
+                                                 else ""))
+        code, ty = dtype_code(q), q.dtype
+        sq, sv = q.shape, v.shape
+        G, dk = sq[-2:]
+        H, dv = sv[-2:]
+        if sv[:-2] != sq[:-2] or G == 0 or H % G:
+            raise ValueError("v must have q's tokens, and a multiple of its "
+                             "heads")
+        L = sq[1] if rank == 4 else 1
+        dims = (sq[0], L, H, G, dk, dv, self._rows("q", q, sq, ty),
+                self._rows("k", k, sq, ty), self._rows("v", v, sv, ty))
+        if log_decay is not None:
+            dense("log_decay", log_decay, sv[:-1], ty, self.device)
+        if head_log_decay is not None:
+            dense("head_log_decay", head_log_decay, (H,), torch.float32,
+                  self.device)
+        if lengths is not None:
+            dense("lengths", lengths, (sq[0],), torch.int32, self.device)
+        return dims, code, dk ** -0.5 if scale is None else scale
 
     def _workspace(self, dims, code, backward):
         """Allocated anew for each call, on its stream: nothing is shared."""
@@ -136,50 +147,59 @@ class LinearAttention:
         import torch
         dims, code, scale = self._inputs(q, k, v, log_decay, head_log_decay,
                                          lengths, scale)
-        b, L, H, _, dk, dv = dims[:6]
-        f32 = torch.float32
-        dense("h0", h0, (b, H, dk, dv), f32, self.device)
-        dense("h_last", h_last, (b, H, dk, dv), f32, self.device)
-        dense("y", y, (b, L, H, dv), q.dtype, self.device)
+        state = (dims[0], dims[2], dims[4], dims[5])
+        dense("h0", h0, state, torch.float32, self.device)
+        dense("h_last", h_last, state, torch.float32, self.device)
+        dense("y", y, v.shape, q.dtype, self.device)
         if h_last is not None and h0 is not None and \
                 h_last.data_ptr() != h0.data_ptr():
             apart(h0=h0, h_last=h_last)
-        with launching(self.device, stream) as s:
-            if y is None:
-                y = torch.empty((b, L, H, dv), dtype=q.dtype,
-                                device=self.device)
-            if h_last is None and return_last_state:
-                h_last = torch.empty((b, H, dk, dv), dtype=f32,
-                                     device=self.device)
-            ws, n = self._workspace(dims, code, False)
-            ssm_linattn_fwd(self.device.index, q, k, v, log_decay,
-                            head_log_decay, scale, lengths, h0, y, h_last, ws,
-                            n, dims, code, s)
+        y, h_last = launch(self.device, stream, self._prompt, q, k, v,
+                           log_decay, head_log_decay, scale, lengths, h0, y,
+                           h_last, return_last_state, dims, code)
         return (y, h_last) if return_last_state else y
+
+    def _prompt(self, s, q, k, v, log_decay, head_log_decay, scale, lengths,
+                h0, y, h_last, want_last, dims, code):
+        import torch
+        if y is None:
+            y = torch.empty(v.shape, dtype=q.dtype, device=self.device)
+        if h_last is None and want_last:
+            h_last = torch.empty((dims[0], dims[2], dims[4], dims[5]),
+                                 dtype=torch.float32, device=self.device)
+        ws, n = self._workspace(dims, code, False)
+        _check(self._lib.ssm_linattn_fwd(
+            self.device.index, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            ptr(log_decay), ptr(head_log_decay), scale, ptr(lengths), ptr(h0),
+            y.data_ptr(), ptr(h_last), ptr(ws), n, ssm_linattn_dims(*dims),
+            code, s), "ssm_linattn_fwd")
+        return y, h_last
 
     def step(self, q, k, v, state, log_decay=None, head_log_decay=None,
              scale=None, y=None, stream=None):
         """One token of every sequence: q, k [b, G, dk], v [b, H, dv],
         log_decay [b, H]. state is updated in place. Returns y [b, H, dv]."""
         import torch
-        if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
-            raise ValueError("q, k and v must have the dimensions "
-                             "[batch, heads, size]")
-        if log_decay is not None:
-            log_decay = log_decay.unsqueeze(1)
-        dims, code, scale = self._inputs(q.unsqueeze(1), k.unsqueeze(1),
-                                         v.unsqueeze(1), log_decay,
-                                         head_log_decay, None, scale)
-        b, _, H, _, dk, dv = dims[:6]
+        dims, code, scale = self._inputs(q, k, v, log_decay, head_log_decay,
+                                         None, scale, rank=3)
         if state is None:
             raise ValueError("state is required")
-        dense("state", state, (b, H, dk, dv), torch.float32, self.device)
-        dense("y", y, (b, H, dv), q.dtype, self.device)
-        with launching(self.device, stream) as s:
-            if y is None:
-                y = torch.empty((b, H, dv), dtype=q.dtype, device=self.device)
-            ssm_linattn_step(self.device.index, q, k, v, log_decay,
-                             head_log_decay, scale, state, y, dims, code, s)
+        dense("state", state, (dims[0], dims[2], dims[4], dims[5]),
+              torch.float32, self.device)
+        dense("y", y, v.shape, q.dtype, self.device)
+        return launch(self.device, stream, self._step, q, k, v, state,
+                      log_decay, head_log_decay, scale, y, dims, code)
+
+    def _step(self, s, q, k, v, state, log_decay, head_log_decay, scale, y,
+              dims, code):
+        import torch
+        if y is None:
+            y = torch.empty(v.shape, dtype=q.dtype, device=self.device)
+        _check(self._lib.ssm_linattn_step(
+            self.device.index, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            ptr(log_decay), ptr(head_log_decay), scale, state.data_ptr(),
+            y.data_ptr(), ssm_linattn_dims(*dims), code, s),
+            "ssm_linattn_step")
         return y
 
     def backward(self, q, k, v, dy, log_decay=None, head_log_decay=None,
@@ -193,29 +213,37 @@ class LinearAttention:
         import torch
         dims, code, scale = self._inputs(q, k, v, log_decay, head_log_decay,
                                          lengths, scale)
-        b, L, H, G, dk, dv = dims[:6]
-        f32 = torch.float32
         if dy is None:
             raise ValueError("dy is required")
-        dense("dy", dy, (b, L, H, dv), q.dtype, self.device)
-        dense("h0", h0, (b, H, dk, dv), f32, self.device)
-        dense("dh_last", dh_last, (b, H, dk, dv), f32, self.device)
-        with launching(self.device, stream) as s:
-            act = dict(dtype=q.dtype, device=self.device)
-            f = dict(dtype=f32, device=self.device)
-            g = dict(
-                dq=torch.empty((b, L, G, dk), **act),
-                dk=torch.empty((b, L, G, dk), **act),
-                dv=torch.empty((b, L, H, dv), **act),
-                dlog_decay=torch.empty((b, L, H), **act)
-                if log_decay is not None and decay_gradient else None,
-                dhead_log_decay=torch.empty((H,), **f)
-                if head_log_decay is not None and decay_gradient else None,
-                dh0=torch.empty((b, H, dk, dv), **f))
-            ws, n = self._workspace(dims, code, True)
-            ssm_linattn_bwd(self.device.index, q, k, v, log_decay,
-                            head_log_decay, scale, lengths, h0, dy, dh_last,
-                            g["dq"], g["dk"], g["dv"], g["dlog_decay"],
-                            g["dhead_log_decay"], g["dh0"], ws, n, dims, code,
-                            s)
+        state = (dims[0], dims[2], dims[4], dims[5])
+        dense("dy", dy, v.shape, q.dtype, self.device)
+        dense("h0", h0, state, torch.float32, self.device)
+        dense("dh_last", dh_last, state, torch.float32, self.device)
+        return launch(self.device, stream, self._backward, q, k, v, dy,
+                      log_decay, head_log_decay, scale, lengths, h0, dh_last,
+                      decay_gradient, dims, code)
+
+    def _backward(self, s, q, k, v, dy, log_decay, head_log_decay, scale,
+                  lengths, h0, dh_last, decay_gradient, dims, code):
+        import torch
+        b, L, H, G, dk, dv = dims[:6]
+        act = dict(dtype=q.dtype, device=self.device)
+        f = dict(dtype=torch.float32, device=self.device)
+        g = dict(
+            dq=torch.empty((b, L, G, dk), **act),
+            dk=torch.empty((b, L, G, dk), **act),
+            dv=torch.empty((b, L, H, dv), **act),
+            dlog_decay=torch.empty((b, L, H), **act)
+            if log_decay is not None and decay_gradient else None,
+            dhead_log_decay=torch.empty((H,), **f)
+            if head_log_decay is not None and decay_gradient else None,
+            dh0=torch.empty((b, H, dk, dv), **f))
+        ws, n = self._workspace(dims, code, True)
+        _check(self._lib.ssm_linattn_bwd(
+            self.device.index, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            ptr(log_decay), ptr(head_log_decay), scale, ptr(lengths), ptr(h0),
+            dy.data_ptr(), ptr(dh_last), g["dq"].data_ptr(),
+            g["dk"].data_ptr(), g["dv"].data_ptr(), ptr(g["dlog_decay"]),
+            ptr(g["dhead_log_decay"]), g["dh0"].data_ptr(), ptr(ws), n,
+            ssm_linattn_dims(*dims), code, s), "ssm_linattn_bwd")
         return g
