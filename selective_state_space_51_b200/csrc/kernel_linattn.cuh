@@ -113,61 +113,94 @@ struct Rows {
   __device__ __forceinline__ bool live(int r) const { return token(r) < len; }
 };
 
-// One [64][COLS] tile of NP bfloat16 planes from `src` (token 0 of the
-// sequence, at the head's first column); rows past the sequence's length and
-// columns past `cols` are zero whatever the memory holds.
-template <typename T, int NP, int COLS>
-__device__ __forceinline__ void load_tile(bf16 *dst, const T *src,
-                                          int64_t stride, int cols,
-                                          const Rows &rows, bool vec) {
-  constexpr int LD = COLS + 8;
-  constexpr int PER = 8;
-  for (int i = threadIdx.x; i < kLaChunk * (COLS / PER); i += 128) {
-    const int r = i / (COLS / PER), c = (i % (COLS / PER)) * PER;
-    uint32_t pl[NP][4];
+constexpr int kThreads = 256;
+
+// A thread's part of one [64][COLS] tile as it lies in memory: COLS / 32
+// groups of 8 elements. All of a chunk's loads are issued before the first is
+// used. Rows past the sequence's length and columns past `cols` are zero
+// whatever the memory holds.
+template <typename T, int COLS>
+struct RawTile {
+  static constexpr int IT = COLS / 32;
+  static constexpr int W = sizeof(T) == 2 ? 1 : 2;  // 16-byte words a group
+  uint4 w[IT][W];
+
+  __device__ __forceinline__ static int row(int i) {
+    return (int(threadIdx.x) + i * kThreads) / (COLS / 8);
+  }
+  __device__ __forceinline__ static int col(int i) {
+    return (int(threadIdx.x) + i * kThreads) % (COLS / 8) * 8;
+  }
+
+  __device__ __forceinline__ void load(const T *src, int64_t stride, int cols,
+                                       const Rows &rows, bool vec) {
 #pragma unroll
-    for (int n = 0; n < NP; ++n)
+    for (int i = 0; i < IT; ++i) {
+      const int r = row(i), c = col(i);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) pl[n][j] = 0u;
-    if (rows.live(r) && c < cols) {
-      const T *s = src + rows.token(r) * stride + c;
-      if constexpr (NP == 1) {
-        if (vec && c + PER <= cols) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4 *>(s));
-          pl[0][0] = v.x; pl[0][1] = v.y; pl[0][2] = v.z; pl[0][3] = v.w;
+      for (int k = 0; k < W; ++k) w[i][k] = make_uint4(0u, 0u, 0u, 0u);
+      if (rows.live(r) && c < cols) {
+        const T *s = src + rows.token(r) * stride + c;
+        if (vec && c + 8 <= cols) {
+#pragma unroll
+          for (int k = 0; k < W; ++k)
+            w[i][k] = __ldg(reinterpret_cast<const uint4 *>(s) + k);
+        } else if constexpr (sizeof(T) == 4) {
+          uint32_t x[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            x[j] = c + j < cols ? __float_as_uint(s[j]) : 0u;
+          w[i][0] = make_uint4(x[0], x[1], x[2], x[3]);
+          w[i][1] = make_uint4(x[4], x[5], x[6], x[7]);
         } else {
-          float x[PER];
+          const uint16_t *h = reinterpret_cast<const uint16_t *>(s);
+          uint32_t x[8];
 #pragma unroll
-          for (int j = 0; j < PER; ++j)
-            x[j] = c + j < cols ? to_f(s[j]) : 0.0f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) pl[0][j] = pack2(x[2 * j], x[2 * j + 1]);
-        }
-      } else {
-        float x[PER];
-        if (vec && c + PER <= cols) {
-          const float4 u = __ldg(reinterpret_cast<const float4 *>(s));
-          const float4 w = __ldg(reinterpret_cast<const float4 *>(s) + 1);
-          x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-          x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
-        } else {
-#pragma unroll
-          for (int j = 0; j < PER; ++j)
-            x[j] = c + j < cols ? to_f(s[j]) : 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t q[NP];
-          split2<NP>(x[2 * j], x[2 * j + 1], q);
-#pragma unroll
-          for (int n = 0; n < NP; ++n) pl[n][j] = q[n];
+          for (int j = 0; j < 8; ++j) x[j] = c + j < cols ? h[j] : 0u;
+          w[i][0] = make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16,
+                               x[4] | x[5] << 16, x[6] | x[7] << 16);
         }
       }
     }
+  }
+
+  // The NP planes of the tile, in shared memory with rows of COLS + 8.
+  template <int NP>
+  __device__ __forceinline__ void store(bf16 *dst) const {
+    constexpr int LD = COLS + 8;
 #pragma unroll
-    for (int n = 0; n < NP; ++n)
-      *reinterpret_cast<uint4 *>(dst + n * kLaChunk * LD + r * LD + c) =
-          make_uint4(pl[n][0], pl[n][1], pl[n][2], pl[n][3]);
+    for (int i = 0; i < IT; ++i) {
+      bf16 *d = dst + row(i) * LD + col(i);
+      if constexpr (NP == 1) {
+        *reinterpret_cast<uint4 *>(d) = w[i][0];
+      } else {
+        const float x[8] = {
+            __uint_as_float(w[i][0].x), __uint_as_float(w[i][0].y),
+            __uint_as_float(w[i][0].z), __uint_as_float(w[i][0].w),
+            __uint_as_float(w[i][1].x), __uint_as_float(w[i][1].y),
+            __uint_as_float(w[i][1].z), __uint_as_float(w[i][1].w)};
+        uint32_t pl[4][NP];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split2<NP>(x[2 * j], x[2 * j + 1], pl[j]);
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+          *reinterpret_cast<uint4 *>(d + n * kLaChunk * LD) =
+              make_uint4(pl[0][n], pl[1][n], pl[2][n], pl[3][n]);
+      }
+    }
+  }
+};
+
+// Brings the rows of a tile to the L2 cache, one chunk ahead of their loads.
+template <typename T>
+__device__ __forceinline__ void prefetch_tile(const T *src, int64_t stride,
+                                              int cols, const Rows &rows) {
+  const int lines = (cols * int(sizeof(T)) + 127) / 128;
+  for (int i = threadIdx.x; i < kLaChunk * lines; i += kThreads) {
+    const int r = i / lines, l = i % lines;
+    if (rows.live(r))
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(
+          src + rows.token(r) * stride + l * (128 / int(sizeof(T)))));
   }
 }
 
@@ -196,8 +229,7 @@ template <typename T>
 __device__ __forceinline__ void load_gates(Gates &g, const LaParams &p,
                                            const Rows &rows, int64_t b,
                                            int h, int reverse) {
-  if (threadIdx.x >= 32) return;
-  const int lane = threadIdx.x;
+  const int lane = threadIdx.x;  // one warp's work
   double c[2];
   int from[2];
   double sum = 0.0;
@@ -271,28 +303,43 @@ struct Layout {
   static constexpr int BYTES = END * 2 + int(sizeof(Gates));
 };
 
-// The state's rows in a warp's accumulators: warp w owns key rows
-// [w QD/4, (w + 1) QD/4) in m-tiles of 16; the usual m16n8 layout.
-template <int QD, class F>
-__device__ __forceinline__ void for_state(F f) {
-  constexpr int MT = QD / 64;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+// The state in the warps' accumulators, in the usual m16n8 layout. With 128
+// key rows a warp owns 16 of them and all 64 columns; with 64, 16 rows and one
+// half of the columns.
+template <int QD>
+struct StateMap {
+  static constexpr int NT = QD == 128 ? 8 : 4;  // n-tiles of a warp
+  __device__ __forceinline__ static int row0() {
+    const int warp = threadIdx.x / 32;
+    return (QD == 128 ? warp : warp % 4) * 16;
+  }
+  __device__ __forceinline__ static int col0() {
+    return QD == 128 ? 0 : int(threadIdx.x) / 128 * 32;
+  }
+  template <class F>
+  __device__ __forceinline__ static void each(F f) {
+    const int lane = threadIdx.x % 32;
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int hrow = 0; hrow < 2; ++hrow)
-        f(m, n, hrow, (warp * MT + m) * 16 + lane / 4 + hrow * 8,
-          n * 8 + (lane % 4) * 2);
-}
+      for (int hr = 0; hr < 2; ++hr)
+        f(n, hr, row0() + lane / 4 + hr * 8, col0() + n * 8 + (lane % 4) * 2);
+  }
+};
 
 // MINB: resident blocks the registers are held to.
+//
+// Warp w computes rows 16 (w % 4).. of y, columns 32 (w / 4)... The tensor
+// cores may truncate where they add to an accumulator, so products of the
+// leading planes go to an accumulator of their own (`hi`), all smaller ones to
+// a second (`lo`): the result then takes a few truncations, not six times as
+// many.
 template <typename T, int NP, int PS, int QD, bool STATE_ONLY, int MINB>
-__global__ void __launch_bounds__(128, MINB)
+__global__ void __launch_bounds__(kThreads, MINB)
     linattn_kernel(const __grid_constant__ LaParams p) {
   using Lay = Layout<T, NP, PS, QD, STATE_ONLY>;
-  constexpr int MT = QD / 64;
+  using Map = StateMap<QD>;
+  constexpr int NT = Map::NT;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   bf16 *sm = reinterpret_cast<bf16 *>(smem_raw);
   bf16 *Ks = sm + Lay::K, *Vs = sm + Lay::V;
@@ -311,6 +358,7 @@ __global__ void __launch_bounds__(128, MINB)
   if (seg >= p.nseg) return;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int wm = warp % 4, wn = warp / 4;
   const int64_t L = p.seqlen;
   int64_t len = L;
   if (p.lengths) {
@@ -339,52 +387,55 @@ __global__ void __launch_bounds__(128, MINB)
   const int64_t bh = b * p.heads + h;
   constexpr int64_t SF = int64_t(QD) * kLaTile;
   float *seg_state =
-      p.nseg > 1 ? job.seg_state +
-                       ((bh * p.nseg + seg) * job.tiles + tile) * SF
-                 : nullptr;
+      p.nseg > 1
+          ? job.seg_state + ((bh * p.nseg + seg) * job.tiles + tile) * SF
+          : nullptr;
 
-  float S[MT][8][4];
+  float S[NT][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) S[m][n][j] = 0.0f;
+    for (int j = 0; j < 4; ++j) S[n][j] = 0.0f;
   if (!STATE_ONLY) {
     if (p.nseg > 1) {
-      for_state<QD>([&](int m, int n, int hr, int row, int col) {
+      Map::each([&](int n, int hr, int row, int col) {
         const float2 v = *reinterpret_cast<const float2 *>(
             seg_state + row * kLaTile + col);
-        S[m][n][2 * hr] = v.x;
-        S[m][n][2 * hr + 1] = v.y;
+        S[n][2 * hr] = v.x;
+        S[n][2 * hr + 1] = v.y;
       });
     } else if (job.init) {
       const float *src = job.init + bh * job.qd * job.vd;
-      for_state<QD>([&](int m, int n, int hr, int row, int col) {
+      Map::each([&](int n, int hr, int row, int col) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           if (row < job.qd && c0 + col + j < job.vd)
-            S[m][n][2 * hr + j] = src[int64_t(row) * job.state_rs +
-                                      int64_t(c0 + col + j) * job.state_cs];
+            S[n][2 * hr + j] = src[int64_t(row) * job.state_rs +
+                                   int64_t(c0 + col + j) * job.state_cs];
       });
     }
   }
 
   float seg_keep = 1.0f;
   const int chunks = int(p.seg_len / kLaChunk);
-  for (int ch = 0; ch < chunks; ++ch) {
+  auto rows_of = [&](int ch) {
     Rows rows;
     const int64_t i0 = int64_t(seg) * p.seg_len + int64_t(ch) * kLaChunk;
     rows.first = job.reverse ? total - 1 - i0 : i0;
     rows.dir = job.reverse ? -1 : 1;
     rows.len = len;
-    const int64_t lowest = job.reverse ? rows.first - (kLaChunk - 1) : i0;
+    return rows;
+  };
+  for (int ch = 0; ch < chunks; ++ch) {
+    const Rows rows = rows_of(ch);
+    const int64_t lowest =
+        job.reverse ? rows.first - (kLaChunk - 1) : rows.first;
     const bool idle = lowest >= len;
     if (idle) {
       // no live step: the state stays, the rows of y behind the sequence are 0
       if (!STATE_ONLY && lowest < L) {
         const int64_t n = L - lowest < kLaChunk ? L - lowest : kLaChunk;
-        for (int64_t i = threadIdx.x; i < n * vcols; i += 128) {
+        for (int64_t i = threadIdx.x; i < n * vcols; i += kThreads) {
           const int64_t t = lowest + i / vcols;
           const int64_t at =
               ((b * L + t) * p.heads + h) * job.vd + c0 + i % vcols;
@@ -397,89 +448,105 @@ __global__ void __launch_bounds__(128, MINB)
       continue;
     }
 
-    __syncthreads();  // the last chunk's reads are done
-    load_gates<T>(gt, p, rows, b, h, job.reverse);
-    load_tile<T, NP, QD>(Ks, kb, job.k_stride, job.qd, rows, kvec);
-    load_tile<T, NP, kLaTile>(Vs, vb, job.v_stride, vcols, rows, vvec);
-    if constexpr (!STATE_ONLY) {
-      load_tile<T, NP, QD>(Qs, qb, job.q_stride, job.qd, rows, qvec);
-      for_state<QD>([&](int m, int n, int hr, int row, int col) {
-        uint32_t pl[PS];
-        split2<PS>(S[m][n][2 * hr], S[m][n][2 * hr + 1], pl);
+    {
+      RawTile<T, QD> rk, rq;
+      RawTile<T, kLaTile> rv;
+      rk.load(kb, job.k_stride, job.qd, rows, kvec);
+      rv.load(vb, job.v_stride, vcols, rows, vvec);
+      if constexpr (!STATE_ONLY)
+        rq.load(qb, job.q_stride, job.qd, rows, qvec);
+      if (ch + 1 < chunks) {
+        const Rows next = rows_of(ch + 1);
+        prefetch_tile(kb, job.k_stride, job.qd, next);
+        prefetch_tile(vb, job.v_stride, vcols, next);
+        if constexpr (!STATE_ONLY)
+          prefetch_tile(qb, job.q_stride, job.qd, next);
+      }
+      __syncthreads();  // the last chunk's reads are done
+      if (warp == 0) load_gates<T>(gt, p, rows, b, h, job.reverse);
+      rk.template store<NP>(Ks);
+      rv.template store<NP>(Vs);
+      if constexpr (!STATE_ONLY) {
+        rq.template store<NP>(Qs);
+        Map::each([&](int n, int hr, int row, int col) {
+          uint32_t pl[PS];
+          split2<PS>(S[n][2 * hr], S[n][2 * hr + 1], pl);
 #pragma unroll
-        for (int s = 0; s < PS; ++s)
-          *reinterpret_cast<uint32_t *>(Ss + s * Lay::TS + row * Lay::LDV +
-                                        col) = pl[s];
-      });
+          for (int s = 0; s < PS; ++s)
+            *reinterpret_cast<uint32_t *>(Ss + s * Lay::TS + row * Lay::LDV +
+                                          col) = pl[s];
+        });
+      }
     }
     __syncthreads();
 
     if constexpr (!STATE_ONLY) {
-      // ---- scores and the state's part: rows 16 warp .. 16 warp + 15
-      float P[8][4], O[8][4];
+      const int r0 = wm * 16 + lane / 4;  // rows r0 and r0 + 8 of this lane
+      // ---- scores: 16 rows, all columns up to the diagonal
+      float P[8][4];
 #pragma unroll
       for (int n = 0; n < 8; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) P[n][j] = O[n][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) P[n][j] = 0.0f;
+      {
+        float lo[NP > 1 ? 8 : 1][4];
+        if constexpr (NP > 1) {
 #pragma unroll
-      for (int ks = 0; ks < QD / 16; ++ks) {
-        uint32_t a[NP][4];
+          for (int n = 0; n < 8; ++n)
 #pragma unroll
-        for (int s = 0; s < NP; ++s)
-          ldsm4(a[s], Qs + s * Lay::TQ + (warp * 16 + lane % 16) * Lay::LDQ +
-                          ks * 16 + (lane / 16) * 8);
-#pragma unroll
-        for (int n2 = 0; n2 < 4; ++n2) {
-          if (n2 <= warp) {
-            uint32_t bk[NP][4];
-#pragma unroll
-            for (int s = 0; s < NP; ++s)
-              ldsm4(bk[s], Ks + s * Lay::TQ +
-                               (n2 * 16 + lane % 8 + (lane / 16) * 8) *
-                                   Lay::LDQ +
-                               ks * 16 + ((lane / 8) % 2) * 8);
-#pragma unroll
-            for (int s = 0; s < NP; ++s)
-#pragma unroll
-              for (int u = 0; u < NP; ++u)
-                if (s + u < 3) {
-                  mma(P[2 * n2], a[s], bk[u][0], bk[u][1]);
-                  mma(P[2 * n2 + 1], a[s], bk[u][2], bk[u][3]);
-                }
-          }
+            for (int j = 0; j < 4; ++j) lo[n][j] = 0.0f;
         }
 #pragma unroll
-        for (int n2 = 0; n2 < 4; ++n2) {
-          uint32_t bs[PS][4];
-#pragma unroll
-          for (int s = 0; s < PS; ++s)
-            ldsm4t(bs[s], Ss + s * Lay::TS +
-                              (ks * 16 + lane % 16) * Lay::LDV + n2 * 16 +
-                              (lane / 16) * 8);
+        for (int ks = 0; ks < QD / 16; ++ks) {
+          uint32_t a[NP][4];
 #pragma unroll
           for (int s = 0; s < NP; ++s)
+            ldsm4(a[s], Qs + s * Lay::TQ + (wm * 16 + lane % 16) * Lay::LDQ +
+                            ks * 16 + (lane / 16) * 8);
 #pragma unroll
-            for (int u = 0; u < PS; ++u)
-              if (s + u < 3) {
-                mma(O[2 * n2], a[s], bs[u][0], bs[u][1]);
-                mma(O[2 * n2 + 1], a[s], bs[u][2], bs[u][3]);
-              }
+          for (int n2 = 0; n2 < 4; ++n2) {
+            if (n2 <= wm) {
+              uint32_t bk[NP][4];
+#pragma unroll
+              for (int s = 0; s < NP; ++s)
+                ldsm4(bk[s], Ks + s * Lay::TQ +
+                                 (n2 * 16 + lane % 8 + (lane / 16) * 8) *
+                                     Lay::LDQ +
+                                 ks * 16 + ((lane / 8) % 2) * 8);
+#pragma unroll
+              for (int s = 0; s < NP; ++s)
+#pragma unroll
+                for (int u = 0; u < NP; ++u) {
+                  if constexpr (NP > 1) {
+                    if (s + u > 0 && s + u < 3) {
+                      mma(lo[2 * n2], a[s], bk[u][0], bk[u][1]);
+                      mma(lo[2 * n2 + 1], a[s], bk[u][2], bk[u][3]);
+                    }
+                  }
+                  if (s + u == 0) {
+                    mma(P[2 * n2], a[0], bk[0][0], bk[0][1]);
+                    mma(P[2 * n2 + 1], a[0], bk[0][2], bk[0][3]);
+                  }
+                }
+            }
+          }
+        }
+        if constexpr (NP > 1) {
+#pragma unroll
+          for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) P[n][j] += lo[n][j];
         }
       }
-      // ---- decay: rows r0 and r0 + 8 of this lane
-      const int r0 = warp * 16 + lane / 4;
+      // ---- decay
 #pragma unroll
       for (int hr = 0; hr < 2; ++hr) {
         const int r = r0 + 8 * hr;
-        const float rd = gt.read[r] * job.si;
         const float chi = gt.hi[r], clo = gt.lo[r];
         const int from = gt.from[r];
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-          // a restart forgets the state whatever it held
-          O[n][2 * hr] = rd == 0.0f ? 0.0f : O[n][2 * hr] * rd;
-          O[n][2 * hr + 1] = rd == 0.0f ? 0.0f : O[n][2 * hr + 1] * rd;
-          if (n < 2 * warp + 2) {
+          if (n < 2 * wm + 2) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const int c = n * 8 + (lane % 4) * 2 + j;
@@ -491,10 +558,65 @@ __global__ void __launch_bounds__(128, MINB)
           }
         }
       }
+      // ---- the state's part, columns 32 wn .. 32 wn + 31
+      constexpr bool OLO = NP > 1 || PS > 1;
+      float O[4][4], lo[OLO ? 4 : 1][4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          O[n][j] = 0.0f;
+          if (OLO) lo[OLO ? n : 0][j] = 0.0f;
+        }
+#pragma unroll
+      for (int ks = 0; ks < QD / 16; ++ks) {
+        uint32_t a[NP][4];
+#pragma unroll
+        for (int s = 0; s < NP; ++s)
+          ldsm4(a[s], Qs + s * Lay::TQ + (wm * 16 + lane % 16) * Lay::LDQ +
+                          ks * 16 + (lane / 16) * 8);
+#pragma unroll
+        for (int n2 = 0; n2 < 2; ++n2) {
+          uint32_t bs[PS][4];
+#pragma unroll
+          for (int s = 0; s < PS; ++s)
+            ldsm4t(bs[s], Ss + s * Lay::TS +
+                              (ks * 16 + lane % 16) * Lay::LDV + wn * 32 +
+                              n2 * 16 + (lane / 16) * 8);
+#pragma unroll
+          for (int s = 0; s < NP; ++s)
+#pragma unroll
+            for (int u = 0; u < PS; ++u) {
+              if constexpr (OLO) {
+                if (s + u > 0 && s + u < 3) {
+                  mma(lo[2 * n2], a[s], bs[u][0], bs[u][1]);
+                  mma(lo[2 * n2 + 1], a[s], bs[u][2], bs[u][3]);
+                }
+              }
+              if (s + u == 0) {
+                mma(O[2 * n2], a[0], bs[0][0], bs[0][1]);
+                mma(O[2 * n2 + 1], a[0], bs[0][2], bs[0][3]);
+              }
+            }
+        }
+      }
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        const float rd = gt.read[r0 + 8 * hr] * job.si;
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int j = 2 * hr; j < 2 * hr + 2; ++j) {
+            // a restart forgets the state whatever it held
+            O[n][j] = rd == 0.0f ? 0.0f : O[n][j] * rd;
+            if constexpr (OLO)
+              lo[n][j] = rd == 0.0f ? 0.0f : lo[n][j] * rd;
+          }
+      }
       // ---- scores times values
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
-        if (kk <= warp) {
+        if (kk <= wm) {
           uint32_t a[PS][4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -505,23 +627,36 @@ __global__ void __launch_bounds__(128, MINB)
             for (int s = 0; s < PS; ++s) a[s][i] = pl[s];
           }
 #pragma unroll
-          for (int n2 = 0; n2 < 4; ++n2) {
+          for (int n2 = 0; n2 < 2; ++n2) {
             uint32_t bv[NP][4];
 #pragma unroll
             for (int s = 0; s < NP; ++s)
               ldsm4t(bv[s], Vs + s * Lay::TV +
-                                (kk * 16 + lane % 16) * Lay::LDV + n2 * 16 +
-                                (lane / 16) * 8);
+                                (kk * 16 + lane % 16) * Lay::LDV + wn * 32 +
+                                n2 * 16 + (lane / 16) * 8);
 #pragma unroll
             for (int s = 0; s < PS; ++s)
 #pragma unroll
-              for (int u = 0; u < NP; ++u)
-                if (s + u < 3) {
-                  mma(O[2 * n2], a[s], bv[u][0], bv[u][1]);
-                  mma(O[2 * n2 + 1], a[s], bv[u][2], bv[u][3]);
+              for (int u = 0; u < NP; ++u) {
+                if constexpr (OLO) {
+                  if (s + u > 0 && s + u < 3) {
+                    mma(lo[2 * n2], a[s], bv[u][0], bv[u][1]);
+                    mma(lo[2 * n2 + 1], a[s], bv[u][2], bv[u][3]);
+                  }
                 }
+                if (s + u == 0) {
+                  mma(O[2 * n2], a[0], bv[0][0], bv[0][1]);
+                  mma(O[2 * n2 + 1], a[0], bv[0][2], bv[0][3]);
+                }
+              }
           }
         }
+      }
+      if constexpr (OLO) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) O[n][j] += lo[n][j];
       }
       // ---- y, and the row dots the decay's gradient is made of
 #pragma unroll
@@ -539,8 +674,8 @@ __global__ void __launch_bounds__(128, MINB)
                             c0
                       : nullptr;
 #pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            const int c = n * 8 + (lane % 4) * 2;
+          for (int n = 0; n < 4; ++n) {
+            const int c = wn * 32 + n * 8 + (lane % 4) * 2;
             const float v0 = live ? O[n][2 * hr] : 0.0f;
             const float v1 = live ? O[n][2 * hr + 1] : 0.0f;
             if (job.y_f32) {
@@ -573,8 +708,8 @@ __global__ void __launch_bounds__(128, MINB)
           dot += __shfl_xor_sync(0xffffffffu, dot, 1);
           dot += __shfl_xor_sync(0xffffffffu, dot, 2);
           if (in && lane % 4 == 0)
-            job.rows[((int64_t(tile) * p.batch + b) * p.heads + h) * L + t] =
-                dot;
+            job.rows[((int64_t(2 * tile + wn) * p.batch + b) * p.heads + h) *
+                         L + t] = dot;
         }
       }
     }
@@ -582,66 +717,70 @@ __global__ void __launch_bounds__(128, MINB)
     // ---- the state: S <- keep S + (weighted k)^T v
     const float keep = gt.keep;
     seg_keep *= keep;
+    float U[NT][4], lo[NT][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          S[m][n][j] = keep == 0.0f ? 0.0f : S[m][n][j] * keep;
+      for (int j = 0; j < 4; ++j) U[n][j] = lo[n][j] = 0.0f;
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
-      float w[4];
+      uint32_t kr[NP][4], a[3][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = gt.write[kk * 16 + (lane % 4) * 2 + (j / 2) * 8 + j % 2] *
-               job.sw;
+      for (int s = 0; s < NP; ++s)
+        ldsm4t(kr[s], Ks + s * Lay::TQ +
+                          (kk * 16 + lane % 8 + (lane / 16) * 8) * Lay::LDQ +
+                          Map::row0() + ((lane / 8) % 2) * 8);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        uint32_t kr[NP][4], a[3][4];
+      for (int i = 0; i < 4; ++i) {
+        float f0 = 0.0f, f1 = 0.0f;
+#pragma unroll
+        for (int s = NP - 1; s >= 0; --s) {
+          f0 += lo2(kr[s][i]);
+          f1 += hi2(kr[s][i]);
+        }
+        const float2 w = *reinterpret_cast<const float2 *>(
+            gt.write + kk * 16 + (lane % 4) * 2 + (i / 2) * 8);
+        uint32_t pl[3];
+        split2<3>(f0 * (w.x * job.sw), f1 * (w.y * job.sw), pl);
+#pragma unroll
+        for (int s = 0; s < 3; ++s) a[s][i] = pl[s];
+      }
+#pragma unroll
+      for (int n2 = 0; n2 < NT / 2; ++n2) {
+        uint32_t bv[NP][4];
 #pragma unroll
         for (int s = 0; s < NP; ++s)
-          ldsm4t(kr[s], Ks + s * Lay::TQ +
-                            (kk * 16 + lane % 8 + (lane / 16) * 8) * Lay::LDQ +
-                            (warp * MT + m) * 16 + ((lane / 8) % 2) * 8);
+          ldsm4t(bv[s], Vs + s * Lay::TV +
+                            (kk * 16 + lane % 16) * Lay::LDV + Map::col0() +
+                            n2 * 16 + (lane / 16) * 8);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float f0 = 0.0f, f1 = 0.0f;
+        for (int s = 0; s < 3; ++s)
 #pragma unroll
-          for (int s = NP - 1; s >= 0; --s) {
-            f0 += lo2(kr[s][i]);
-            f1 += hi2(kr[s][i]);
+          for (int u = 0; u < NP; ++u) {
+            if (s + u > 0 && s + u < 3) {
+              mma(lo[2 * n2], a[s], bv[u][0], bv[u][1]);
+              mma(lo[2 * n2 + 1], a[s], bv[u][2], bv[u][3]);
+            }
+            if (s + u == 0) {
+              mma(U[2 * n2], a[0], bv[0][0], bv[0][1]);
+              mma(U[2 * n2 + 1], a[0], bv[0][2], bv[0][3]);
+            }
           }
-          uint32_t pl[3];
-          split2<3>(f0 * w[(i / 2) * 2], f1 * w[(i / 2) * 2 + 1], pl);
-#pragma unroll
-          for (int s = 0; s < 3; ++s) a[s][i] = pl[s];
-        }
-#pragma unroll
-        for (int n2 = 0; n2 < 4; ++n2) {
-          uint32_t bv[NP][4];
-#pragma unroll
-          for (int s = 0; s < NP; ++s)
-            ldsm4t(bv[s], Vs + s * Lay::TV +
-                              (kk * 16 + lane % 16) * Lay::LDV + n2 * 16 +
-                              (lane / 16) * 8);
-#pragma unroll
-          for (int s = 0; s < 3; ++s)
-#pragma unroll
-            for (int u = 0; u < NP; ++u)
-              if (s + u < 3) {
-                mma(S[m][2 * n2], a[s], bv[u][0], bv[u][1]);
-                mma(S[m][2 * n2 + 1], a[s], bv[u][2], bv[u][3]);
-              }
-        }
       }
     }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float u = U[n][j] + lo[n][j];
+        S[n][j] = keep == 0.0f ? u : fmaf(keep, S[n][j], u);
+      }
   }
 
   if constexpr (STATE_ONLY) {
-    for_state<QD>([&](int m, int n, int hr, int row, int col) {
+    Map::each([&](int n, int hr, int row, int col) {
       *reinterpret_cast<float2 *>(seg_state + row * kLaTile + col) =
-          make_float2(S[m][n][2 * hr], S[m][n][2 * hr + 1]);
+          make_float2(S[n][2 * hr], S[n][2 * hr + 1]);
     });
     if (tile == 0 && threadIdx.x == 0)
       job.seg_decay[bh * p.nseg + seg] = seg_keep;
@@ -651,13 +790,13 @@ __global__ void __launch_bounds__(128, MINB)
     if (job.reverse && len > 0)
       f = ex2_d(gate_at<T>(p, b, 0, h) * 1.4426950408889634);
     float *dst = job.last + bh * job.qd * job.vd;
-    for_state<QD>([&](int m, int n, int hr, int row, int col) {
+    Map::each([&](int n, int hr, int row, int col) {
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         if (row < job.qd && c0 + col + j < job.vd)
           dst[int64_t(row) * job.state_rs +
               int64_t(c0 + col + j) * job.state_cs] =
-              f == 0.0f ? 0.0f : S[m][n][2 * hr + j] * f;
+              f == 0.0f ? 0.0f : S[n][2 * hr + j] * f;
     });
   }
 }
@@ -774,7 +913,7 @@ __global__ void __launch_bounds__(256)
     const int64_t t = hi - 1 - threadIdx.x;
     float v = 0.0f;
     if (t >= t0 && t < len)
-      for (int k = 0; k < p.tiles; ++k) {
+      for (int k = 0; k < p.parts; ++k) {
         const int64_t at = ((int64_t(k) * p.batch + b) * p.heads + h) * L + t;
         v += p.rows_q[at] - p.rows_k[at];
       }

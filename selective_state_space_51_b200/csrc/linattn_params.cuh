@@ -31,7 +31,8 @@ struct LaJob {
   const void *dot;                       // row-dot operand [.., vd] or nullptr
   int64_t dot_stride;
   int dot_heads;
-  float *rows;                           // [tiles, b, heads, L] row dots
+  float *rows;                           // [2 tiles, b, heads, L] row dots,
+                                         // of 32 columns each
   float *seg_state;                      // [b, heads, nseg, tiles, QD, 64]
   float *seg_decay;                      // [b, heads, nseg]
 };
@@ -51,7 +52,7 @@ struct LaParams {
 // ends.
 struct LaGateParams {
   const float *rows_q, *rows_k;  // row dots of dq with q, of dk with k
-  int tiles;
+  int parts;                           // of 32 columns each
   const float *fwd_state, *rev_state;  // seg_state of the dq and dk passes
   int64_t state_floats;                // floats of one (segment, all tiles)
   const float *last_state, *dh_last;   // [b, H, dk, dv], dh_last or nullptr

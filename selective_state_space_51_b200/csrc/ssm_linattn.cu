@@ -90,7 +90,7 @@ void cut(Plan *pl, int64_t blocks, int64_t L, int sms, int per_sm,
   pl->nseg = int(ceil_div(chunks, per));
 }
 
-int resident(int dtype) { return dtype == SSM_BF16 ? 3 : 2; }
+int resident(int) { return 2; }
 
 Plan plan_fwd(const ssm_linattn_dims &d, int dtype, int sms) {
   Plan pl;
@@ -125,8 +125,8 @@ Plan plan_bwd(const ssm_linattn_dims &d, int dtype, bool gate, int sms) {
     pl.part_dk = take(&pl.bytes, bh * d.seqlen * d.dk);
   }
   if (gate) {
-    pl.rows_q = take(&pl.bytes, bh * d.seqlen * tk);
-    pl.rows_k = take(&pl.bytes, bh * d.seqlen * tk);
+    pl.rows_q = take(&pl.bytes, bh * d.seqlen * 2 * tk);
+    pl.rows_k = take(&pl.bytes, bh * d.seqlen * 2 * tk);
     pl.part_head = take(&pl.bytes, bh * pl.nseg);
     pl.last = take(&pl.bytes, bh * d.dk * d.dv);
   }
@@ -136,8 +136,7 @@ Plan plan_bwd(const ssm_linattn_dims &d, int dtype, bool gate, int sms) {
 // Every job of `p` (n of them), which share QD and PS.
 template <typename T, int NP, int PS, int QD>
 int launch_jobs(const LaParams &p, int n, cudaStream_t s) {
-  constexpr int MINB = NP == 3 ? (QD == 64 ? 2 : 1)
-                               : (QD == 64 || PS == 1 ? 3 : 2);
+  constexpr int MINB = NP == 3 && QD == 128 ? 1 : 2;
   int tiles = 0;
   for (int j = 0; j < n; ++j) tiles = std::max(tiles, p.job[j].tiles);
   // jobs of one launch have the same tile count (the caller groups them)
@@ -151,7 +150,8 @@ int launch_jobs(const LaParams &p, int n, cudaStream_t s) {
       cudaGetLastError();
       return SSM_ERR_CUDA;
     }
-    kern<<<dim3(unsigned(one * (p.nseg - 1)), n), 128, smem, s>>>(p);
+    kern<<<dim3(unsigned(one * (p.nseg - 1)), n),
+           ssm::la::kThreads, smem, s>>>(p);
     if (cudaGetLastError() != cudaSuccess) return SSM_ERR_CUDA;
     const int64_t el = int64_t(QD) * ssm::kLaTile * one;
     if (ceil_div(el, 256) > 0x7fffffff) return SSM_ERR_UNSUPPORTED;
@@ -166,7 +166,8 @@ int launch_jobs(const LaParams &p, int n, cudaStream_t s) {
     cudaGetLastError();
     return SSM_ERR_CUDA;
   }
-  kern<<<dim3(unsigned(one * p.nseg), n), 128, smem, s>>>(p);
+  kern<<<dim3(unsigned(one * p.nseg), n),
+           ssm::la::kThreads, smem, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
 
@@ -428,7 +429,7 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
     LaGateParams g{};
     g.rows_q = at(pl.rows_q);
     g.rows_k = at(pl.rows_k);
-    g.tiles = jq.tiles;
+    g.parts = 2 * jq.tiles;
     if (pl.nseg > 1) {
       g.fwd_state = at(pl.state[0]);
       g.rev_state = at(pl.state[1]);
