@@ -128,6 +128,15 @@ SSM_API int ssm_linattn_bwd(int device, const void *q, const void *k,
                             ssm_linattn_dims dims, int dtype,
                             struct CUstream_st *stream);
 
+/*
+ * ssm_linattn_sync_status: wait for `stream`, then report whether a bounded
+ * wait inside a kernel of ssm_linattn_fwd or ssm_linattn_bwd gave up on
+ * `device` since the previous report (SSM_ERR_TIMEOUT: the results of those
+ * calls are invalid; no input leads there), SSM_ERR_CUDA on an asynchronous
+ * CUDA error, else SSM_OK. Resets the status, which all streams share.
+ */
+SSM_API int ssm_linattn_sync_status(int device, struct CUstream_st *stream);
+
 #ifdef __cplusplus
 }
 #endif

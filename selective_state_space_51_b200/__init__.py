@@ -145,6 +145,8 @@ def library() -> ctypes.CDLL:
                 i32, vp, vp, vp, vp, vp, ctypes.c_float] + [vp] * 11 + [
                 ctypes.c_size_t, dims, i32, vp]
             lib.ssm_linattn_bwd.restype = i32
+            lib.ssm_linattn_sync_status.argtypes = [i32, vp]
+            lib.ssm_linattn_sync_status.restype = i32
             i64 = ctypes.c_int64
             lib.ssm_layernorm_workspace.argtypes = [
                 i32, i64, i64, i32, ctypes.POINTER(ctypes.c_size_t)]
@@ -468,4 +470,4 @@ from .layernorm import (LayerNorm, ssm_layernorm_bwd,  # noqa: E402,F401
                         ssm_layernorm_fwd, ssm_layernorm_workspace)
 from .linattn import (LinearAttention, ssm_linattn_bwd,  # noqa: E402,F401
                       ssm_linattn_fwd, ssm_linattn_step,
-                      ssm_linattn_workspace)
+                      ssm_linattn_sync_status, ssm_linattn_workspace)

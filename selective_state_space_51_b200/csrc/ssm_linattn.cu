@@ -5,10 +5,12 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "../../include/ssm_linattn.h"
 #include "device_info.cuh"
-#include "kernel_linattn.cuh"
+#include "kernel_linattn_tc.cuh"
+#include "tensor_map.cuh"
 
 namespace {
 
@@ -23,9 +25,10 @@ constexpr int64_t kMaxElements = int64_t(1) << 56;
 // The decay's gradient sums differences inside a segment: a bounded segment
 // bounds how many of them are added up.
 constexpr int64_t kGateSegment = 1024;
-// Shortest segment a sequence is split into: the state a segment hands over
-// is worth about two chunks' bytes.
-constexpr int64_t kMinSegment = 256;
+
+// Shared memory that lets one block of the tensor-memory kernel (which takes
+// all of TMEM) onto an SM at a time.
+constexpr int kOnePerSm = 120 * 1024;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int key_pad(int64_t d) { return d <= 64 ? 64 : 128; }
@@ -57,6 +60,10 @@ int check_dims(ssm_linattn_dims *d, int dtype, int64_t max_value) {
   return SSM_OK;
 }
 
+// Which kernel runs a call's passes: the tensor-memory kernel takes bfloat16
+// rows on 16-byte boundaries, the other one everything.
+enum class Path { kAny, kTc };
+
 struct Plan {
   int nseg = 1;
   int64_t seg_len = 0;
@@ -77,26 +84,25 @@ size_t take(size_t *at, size_t floats) {
 // of the GPU idle, a sequence is cut so that about `per_sm` blocks are there
 // for each SM. The states in front of the segments cost one more reading of k
 // and v, so a grid that fills the GPU by itself is not cut.
-void cut(Plan *pl, int64_t blocks, int64_t L, int sms, int per_sm,
+void cut(Plan *pl, int64_t blocks, int64_t L, int sms, Path path,
          int64_t most) {
-  const int64_t slots = int64_t(sms) * per_sm;
+  const int chunk = path == Path::kTc ? ssm::lat::kChunk : ssm::kLaChunk;
+  const int64_t slots = int64_t(sms) * (path == Path::kTc ? 1 : 2);
   int64_t n = 1;
   if (blocks * 2 <= slots)
-    n = std::min(slots / blocks, std::max<int64_t>(1, L / kMinSegment));
+    n = std::min(slots / blocks, std::max<int64_t>(1, L / (4 * chunk)));
   n = std::max(n, ceil_div(L, most));
-  const int64_t chunks = ceil_div(L, ssm::kLaChunk);
+  const int64_t chunks = ceil_div(L, chunk);
   const int64_t per = ceil_div(chunks, n);
-  pl->seg_len = per * ssm::kLaChunk;
+  pl->seg_len = per * chunk;
   pl->nseg = int(ceil_div(chunks, per));
 }
 
-int resident(int) { return 2; }
-
-Plan plan_fwd(const ssm_linattn_dims &d, int dtype, int sms) {
+Plan plan_fwd(const ssm_linattn_dims &d, Path path, int sms) {
   Plan pl;
   const int64_t tiles = ceil_div(d.dv, ssm::kLaTile);
-  cut(&pl, d.batch * d.heads * tiles, d.seqlen, sms, resident(dtype),
-      int64_t(1) << 40);
+  cut(&pl, d.batch * d.heads * (path == Path::kTc ? 1 : tiles), d.seqlen, sms,
+      path, int64_t(1) << 40);
   if (pl.nseg > 1) {
     const size_t bh = size_t(d.batch) * d.heads;
     pl.state[0] = take(&pl.bytes, bh * pl.nseg * tiles * key_pad(d.dk) *
@@ -106,13 +112,13 @@ Plan plan_fwd(const ssm_linattn_dims &d, int dtype, int sms) {
   return pl;
 }
 
-Plan plan_bwd(const ssm_linattn_dims &d, int dtype, bool gate, int sms) {
+Plan plan_bwd(const ssm_linattn_dims &d, Path path, bool gate, int sms) {
   Plan pl;
   const int64_t tk = ceil_div(d.dk, ssm::kLaTile),
                 tv = ceil_div(d.dv, ssm::kLaTile);
   const size_t bh = size_t(d.batch) * d.heads;
-  cut(&pl, d.batch * d.heads * (2 * tk + tv), d.seqlen, sms, resident(dtype),
-      gate ? kGateSegment : int64_t(1) << 40);
+  cut(&pl, d.batch * d.heads * (path == Path::kTc ? 3 : 2 * tk + tv),
+      d.seqlen, sms, path, gate ? kGateSegment : int64_t(1) << 40);
   if (pl.nseg > 1)
     for (int j = 0; j < 3; ++j) {
       pl.state[j] = take(&pl.bytes, bh * pl.nseg * (j < 2 ? tk : tv) *
@@ -183,6 +189,116 @@ int run_jobs(const LaParams &p, int n, int dtype, bool exact, cudaStream_t s) {
                   : launch_jobs<bf16, 1, 1, 128>(p, n, s);
 }
 
+// ---- the tensor-memory kernel
+__device__ int g_linattn_status;
+
+int *status_word(int device) {
+  static std::atomic<int *> known[64];
+  int *w = known[device].load(std::memory_order_relaxed);
+  if (!w) {
+    void *q = nullptr;
+    if (cudaGetSymbolAddress(&q, g_linattn_status) != cudaSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    w = static_cast<int *>(q);
+    known[device].store(w, std::memory_order_relaxed);
+  }
+  return w;
+}
+
+bool tc_rows(const void *q, int64_t stride, int64_t d) {
+  return aligned(q, 16) && stride % 8 == 0 && d % 8 == 0 &&
+         stride < (int64_t(1) << 36);
+}
+
+// Whether every pass of a call can run there.
+bool tc_takes(const ssm_linattn_dims &d, int dtype, const void *q,
+              const void *k, const void *v,
+              std::initializer_list<const void *> dense) {
+  if (dtype != SSM_BF16 || d.dv > 128 || d.seqlen >= (int64_t(1) << 31) ||
+      d.batch >= (int64_t(1) << 31) || !tc_rows(q, d.q_stride, d.dk) ||
+      !tc_rows(k, d.k_stride, d.dk) || !tc_rows(v, d.v_stride, d.dv) ||
+      d.seqlen * d.q_stride >= (int64_t(1) << 38) ||
+      d.seqlen * d.k_stride >= (int64_t(1) << 38) ||
+      d.seqlen * d.v_stride >= (int64_t(1) << 38) ||
+      d.seqlen * d.heads * d.dv >= (int64_t(1) << 38))
+    return false;
+  for (const void *a : dense)
+    if (a && !aligned(a, 16)) return false;
+  return true;
+}
+
+template <int QD, int TV, int PS>
+int launch_tc(const ssm::lat::Params &pp, int n, cudaStream_t s) {
+  const LaParams &p = pp.p;
+  const int64_t one = int64_t(p.heads) * p.batch;
+  if (one > 0x7fffffff / p.nseg) return SSM_ERR_UNSUPPORTED;
+  if (p.nseg > 1) {
+    auto kern = ssm::lat::linattn_tc_kernel<QD, TV, 1, true>;
+    constexpr int smem = ssm::lat::Lay<QD, TV, 1, true>::BYTES;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem < kOnePerSm ? kOnePerSm : smem) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return SSM_ERR_CUDA;
+    }
+    kern<<<dim3(unsigned(one * (p.nseg - 1)), n), ssm::lat::kThreads,
+           smem < kOnePerSm ? kOnePerSm : smem, s>>>(pp);
+    if (cudaGetLastError() != cudaSuccess) return SSM_ERR_CUDA;
+    int tiles = 0;
+    for (int j = 0; j < n; ++j) tiles = std::max(tiles, p.job[j].tiles);
+    const int64_t el = int64_t(QD) * ssm::kLaTile * one * tiles;
+    if (ceil_div(el, 256) > 0x7fffffff) return SSM_ERR_UNSUPPORTED;
+    ssm::la::linattn_join_kernel<QD>
+        <<<dim3(unsigned(ceil_div(el, 256)), n), 256, 0, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return SSM_ERR_CUDA;
+  }
+  auto kern = ssm::lat::linattn_tc_kernel<QD, TV, PS, false>;
+  constexpr int need = ssm::lat::Lay<QD, TV, PS, false>::BYTES;
+  constexpr int smem = need < kOnePerSm ? kOnePerSm : need;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           smem) != cudaSuccess) {
+    cudaGetLastError();
+    return SSM_ERR_CUDA;
+  }
+  kern<<<dim3(unsigned(one * p.nseg), n), ssm::lat::kThreads, smem, s>>>(pp);
+  return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
+}
+
+// Two planes of the state and the scores do not fit beside two 128-wide
+// stages.
+bool tc_exact_fits(int64_t key, int64_t value) {
+  return key <= 64 || value <= 64;
+}
+
+// The jobs of `p` (n of them), which share their sizes and PS.
+int run_tc(const LaParams &p, int n, bool exact, int device, cudaStream_t s) {
+  ssm::lat::Params pp{};
+  pp.p = p;
+  pp.status = status_word(device);
+  if (!pp.status) return SSM_ERR_CUDA;
+  for (int i = 0; i < n; ++i) {
+    const LaJob &j = p.job[i];
+    if (!ssm::row_map(&pp.map[i][0], j.q, p.batch, p.seqlen, j.q_heads, j.qd,
+                      j.q_stride, ssm::lat::kChunk) ||
+        !ssm::row_map(&pp.map[i][1], j.k, p.batch, p.seqlen, j.k_heads, j.qd,
+                      j.k_stride, ssm::lat::kChunk) ||
+        !ssm::row_map(&pp.map[i][2], j.v, p.batch, p.seqlen, j.v_heads, j.vd,
+                      j.v_stride, ssm::lat::kChunk))
+      return SSM_ERR_CUDA;
+  }
+  const bool q64 = p.job[0].qd <= 64, v64 = p.job[0].vd <= 64;
+  if (exact)
+    return q64 ? (v64 ? launch_tc<64, 64, 2>(pp, n, s)
+                      : launch_tc<64, 128, 2>(pp, n, s))
+               : launch_tc<128, 64, 2>(pp, n, s);
+  return q64 ? (v64 ? launch_tc<64, 64, 1>(pp, n, s)
+                    : launch_tc<64, 128, 1>(pp, n, s))
+             : (v64 ? launch_tc<128, 64, 1>(pp, n, s)
+                    : launch_tc<128, 128, 1>(pp, n, s));
+}
+
 bool check_floats(std::initializer_list<const float *> list) {
   for (const float *q : list)
     if (q && !aligned(q, 4)) return false;
@@ -228,9 +344,15 @@ int ssm_linattn_workspace(int device, ssm_linattn_dims dims, int dtype,
   int sms = 0;
   rc = ssm::device_sms(device, &sms);
   if (rc != SSM_OK) return rc;
-  *bytes = backward ? std::max(plan_bwd(dims, dtype, true, sms).bytes,
-                               plan_bwd(dims, dtype, false, sms).bytes)
-                    : plan_fwd(dims, dtype, sms).bytes;
+  for (Path path : {Path::kAny, Path::kTc}) {
+    if (path == Path::kTc && (dtype != SSM_BF16 || dims.dv > 128)) continue;
+    if (backward) {
+      for (bool gate : {false, true})
+        *bytes = std::max(*bytes, plan_bwd(dims, path, gate, sms).bytes);
+    } else {
+      *bytes = std::max(*bytes, plan_fwd(dims, path, sms).bytes);
+    }
+  }
   return SSM_OK;
 }
 
@@ -255,7 +377,9 @@ int ssm_linattn_fwd(int device, const void *q, const void *k, const void *v,
   int sms = 0;
   rc = ssm::device_ready(device, &sms);
   if (rc != SSM_OK) return rc;
-  const Plan pl = plan_fwd(dims, dtype, sms);
+  const Path path =
+      tc_takes(dims, dtype, q, k, v, {y}) ? Path::kTc : Path::kAny;
+  const Plan pl = plan_fwd(dims, path, sms);
   if (pl.bytes > workspace_bytes || (pl.bytes && !workspace))
     return SSM_ERR_INVALID;
   if (workspace && !aligned(workspace, 16)) return SSM_ERR_ALIGN;
@@ -277,7 +401,9 @@ int ssm_linattn_fwd(int device, const void *q, const void *k, const void *v,
     j.seg_state = reinterpret_cast<float *>(ws + pl.state[0]);
     j.seg_decay = reinterpret_cast<float *>(ws + pl.decay[0]);
   }
-  return run_jobs(p, 1, dtype, false, reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return path == Path::kTc ? run_tc(p, 1, false, device, s)
+                           : run_jobs(p, 1, dtype, false, s);
 }
 
 int ssm_linattn_step(int device, const void *q, const void *k, const void *v,
@@ -349,7 +475,11 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
   rc = ssm::device_ready(device, &sms);
   if (rc != SSM_OK) return rc;
   const bool gate = dlog_decay || dhead_log_decay;
-  const Plan pl = plan_bwd(dims, dtype, gate, sms);
+  const Path path = tc_takes(dims, dtype, q, k, v, {dy, dq, dk, dv}) &&
+                            (!gate || tc_exact_fits(dims.dv, dims.dk))
+                        ? Path::kTc
+                        : Path::kAny;
+  const Plan pl = plan_bwd(dims, path, gate, sms);
   if (pl.bytes > workspace_bytes || (pl.bytes && !workspace))
     return SSM_ERR_INVALID;
   if (workspace && !aligned(workspace, 16)) return SSM_ERR_ALIGN;
@@ -409,10 +539,14 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
   LaParams p = common(dims, pl, log_decay, head_log_decay, lengths);
   p.job[0] = jq;
   p.job[1] = jk;
-  rc = run_jobs(p, 2, dtype, gate, s);
+  auto run = [&](int n, bool exact) {
+    return path == Path::kTc ? run_tc(p, n, exact, device, s)
+                             : run_jobs(p, n, dtype, exact, s);
+  };
+  rc = run(2, gate);
   if (rc != SSM_OK) return rc;
   p.job[0] = jv;
-  rc = run_jobs(p, 1, dtype, false, s);
+  rc = run(1, false);
   if (rc != SSM_OK) return rc;
 
   if (shared) {
@@ -429,7 +563,8 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
     LaGateParams g{};
     g.rows_q = at(pl.rows_q);
     g.rows_k = at(pl.rows_k);
-    g.parts = 2 * jq.tiles;
+    // each pass leaves its row dots in parts of its columns
+    g.parts = path == Path::kTc ? 2 : 2 * jq.tiles;
     if (pl.nseg > 1) {
       g.fwd_state = at(pl.state[0]);
       g.rev_state = at(pl.state[1]);
@@ -457,6 +592,28 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
     if (cudaGetLastError() != cudaSuccess) return SSM_ERR_CUDA;
   }
   return SSM_OK;
+}
+
+int ssm_linattn_sync_status(int device, struct CUstream_st *stream) {
+  int sms = 0;
+  int rc = ssm::device_ready(device, &sms);
+  if (rc != SSM_OK) return rc;
+  int *word = status_word(device);
+  if (!word || cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) !=
+                   cudaSuccess) {
+    cudaGetLastError();
+    return SSM_ERR_CUDA;
+  }
+  int value = 0;
+  if (cudaMemcpy(&value, word, sizeof(int), cudaMemcpyDeviceToHost) !=
+      cudaSuccess)
+    return SSM_ERR_CUDA;
+  if (value == 0) return SSM_OK;
+  value = 0;
+  if (cudaMemcpy(word, &value, sizeof(int), cudaMemcpyHostToDevice) !=
+      cudaSuccess)
+    return SSM_ERR_CUDA;
+  return SSM_ERR_TIMEOUT;
 }
 
 }  // extern "C"

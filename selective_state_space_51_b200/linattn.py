@@ -61,6 +61,11 @@ def ssm_linattn_bwd(device, q, k, v, log_decay, head_log_decay, scale, lengths,
     return _check(rc, "ssm_linattn_bwd") if check else rc
 
 
+def ssm_linattn_sync_status(device=0, stream=None) -> int:
+    """Status code (not raised): SSM_OK, SSM_ERR_TIMEOUT or SSM_ERR_CUDA."""
+    return library().ssm_linattn_sync_status(int(device), _stream(stream))
+
+
 class LinearAttention:
     """Linear attention with a decay for each head, on one device.
 
@@ -138,6 +143,12 @@ class LinearAttention:
         if n == 0:
             return None, 0
         return torch.empty(n, dtype=torch.uint8, device=self.device), n
+
+    def sync_status(self, stream=None) -> int:
+        """Waits for the stream; SSM_OK unless a kernel's bounded wait gave
+        up or the device has an error."""
+        return launch(self.device, stream, lambda s: ssm_linattn_sync_status(
+            self.device.index, s))
 
     def __call__(self, q, k, v, log_decay=None, head_log_decay=None,
                  scale=None, lengths=None, h0=None, y=None, h_last=None,
