@@ -285,7 +285,10 @@ int run_tc(const LaParams &p, int n, bool exact, int device, cudaStream_t s) {
         !ssm::row_map(&pp.map[i][1], j.k, p.batch, p.seqlen, j.k_heads, j.qd,
                       j.k_stride, ssm::lat::kChunk) ||
         !ssm::row_map(&pp.map[i][2], j.v, p.batch, p.seqlen, j.v_heads, j.vd,
-                      j.v_stride, ssm::lat::kChunk))
+                      j.v_stride, ssm::lat::kChunk) ||
+        (!j.y_f32 &&
+         !ssm::row_map(&pp.map[i][3], j.y, p.batch, p.seqlen, p.heads, j.vd,
+                       int64_t(p.heads) * j.vd, ssm::lat::kChunk)))
       return SSM_ERR_CUDA;
   }
   const bool q64 = p.job[0].qd <= 64, v64 = p.job[0].vd <= 64;
@@ -563,8 +566,8 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
     LaGateParams g{};
     g.rows_q = at(pl.rows_q);
     g.rows_k = at(pl.rows_k);
-    // each pass leaves its row dots in parts of its columns
-    g.parts = path == Path::kTc ? 2 : 2 * jq.tiles;
+    // the other kernel's passes leave row dots for each 32 columns
+    g.parts = path == Path::kTc ? 1 : 2 * jq.tiles;
     if (pl.nseg > 1) {
       g.fwd_state = at(pl.state[0]);
       g.rev_state = at(pl.state[1]);

@@ -47,8 +47,22 @@ constexpr unsigned kPolls = 1000u * 1000u;
 
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity,
                                          volatile int *dead, int *status) {
+#pragma unroll 1
   for (unsigned i = 0; i < kPolls; ++i) {
     if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
+    if (*dead) return false;
+  }
+  *dead = 1;
+  *status = 1;
+  return false;
+}
+
+// The same for one thread on its own.
+__device__ __forceinline__ bool bar_wait_one(uint32_t bar, uint32_t parity,
+                                             volatile int *dead, int *status) {
+#pragma unroll 1
+  for (unsigned i = 0; i < kPolls; ++i) {
+    if (bar_try(bar, parity)) return true;
     if (*dead) return false;
   }
   *dead = 1;
@@ -176,6 +190,32 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map,
       "bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
       "l"(map), "r"(bar), "r"(x), "r"(head), "r"(token), "r"(batch)
       : "memory");
+}
+
+__device__ __forceinline__ void store_box(const CUtensorMap *map, uint32_t src,
+                                          int x, int head, int token,
+                                          int batch) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, "
+      "%3, %4, %5}], [%1];" ::"l"(map),
+      "r"(src), "r"(x), "r"(head), "r"(token), "r"(batch)
+      : "memory");
+}
+// Waits until this thread's stores have read their shared memory.
+__device__ __forceinline__ void store_read() {
+  asm volatile("cp.async.bulk.commit_group;\n"
+               "cp.async.bulk.wait_group.read 0;" ::
+                   : "memory");
+}
+
+// The registers of a warpgroup's threads from here on.
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 }  // namespace tc
