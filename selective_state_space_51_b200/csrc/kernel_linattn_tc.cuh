@@ -14,12 +14,16 @@
 // state's transpose lies in the same lanes (one value column a lane) as the
 // product that is added to it. They go through two buffers of 32 steps.
 //
-// One warpgroup each (a thread has one TMEM lane): 0 turns P into P', 1 weighs
-// the values and holds the state, 2 scales O1 in its place (O2 is added to it
-// there) and hands y to a TMA store.
-// Of the fourth, warp 12 moves q, k, v (two chunks deep) and y, 13 issues the
-// products, 14 and 15 sum the decays ahead of their chunks. Everything between them goes
-// through mbarriers with bounded waits; the registers are divided by need.
+// Three warpgroups (a thread has one TMEM lane) share the chunk's 128 weighted
+// steps, which all need the same arithmetic, and have one task of their own
+// each: the first turns P into P', the second holds the state, the third
+// scales O1 in its place (O2 is added to it there) and hands y to a TMA store.
+// The weighted values pass through three buffers of 32, 32 and 16 steps, so
+// that the first 80 steps of a chunk are ready while the state of the last one
+// is still being added up. Of the fourth warpgroup, warp 12 moves q, k, v (two
+// chunks deep) and y, 13 issues the products, 14 and 15 sum the decays ahead
+// of their chunks. Everything between them goes through mbarriers with bounded
+// waits; the registers are divided by need.
 //
 // The decay e^{c_i - c_j}: outside the 32 x 32 blocks on the diagonal it is
 // e^{c_i - c_r} e^{c_r - c_j}, r the last step of j's block: both factors are
@@ -42,20 +46,6 @@ struct Params {
   int *status;
 };
 
-// The decays of a chunk; arrays by row (token order). Steps are counted in
-// the order of time, which in reverse is from the last row.
-struct Gates {
-  float hi[kChunk], lo[kChunk];  // c since the last restart
-  float near[kChunk];            // e^{c_r - c_j}, r: the last step of j's 32
-  float read[kChunk];            // si e^{c_i}, 0 behind a restart
-  float write[kChunk];           // sw e^{c_C - c_i}, 0 before a restart
-  unsigned char from[kChunk];    // the last restart at or before the step
-  float keep;
-  int dead;
-  uint32_t tmem;
-  uint64_t bars[26];
-};
-
 enum Bar {
   kFull0, kFull1,      // q, k, v of a stage have arrived
   kEmpty0, kEmpty1,    // the stage's products are done
@@ -63,20 +53,56 @@ enum Bar {
   kRead,               // O1
   kOut,                // O2
   kUpdate,             // U
-  kWEmpty0, kWEmpty1,  // a buffer of weighted values has been used
-  kGatesA, kGatesB, kGatesC,  // hi, lo, near, from; write, keep; read
+  kUsed,               // (3) a buffer of weighted values has been used
+  kGates = kUsed + 3,  // hi, lo, near, from
+  kWeights0, kWeights1,  // write, keep of every second chunk
   kStored,             // y has been read by its store
-  kSingle,             // (barriers above: one arrival; below: a warpgroup's)
-  kWFull0 = kSingle, kWFull1,
-  kScored,             // P'
-  kReadDone,           // O1 read
+  // the barriers above take one arrival, these a warpgroup's ...
+  kWeighed,            // (5) a slot of weighted values is there
+  kScored = kWeighed + 5,  // P'
+  kReadDone,           // O1 scaled
   kOutRead,            // O2 read
   kState,              // S stored, U read
-  kFreeA, kFreeB, kFreeC,
   kStaged,             // y in shared memory
   kClean,              // rows behind the sequence's end zeroed
-  kFin,                // (one arrival)
+  kGatesFree,          // ... two warpgroups' ...
+  kWeightsFree0, kWeightsFree1,  // ... and three
+  kFin,                // one
+  kBars
 };
+
+// The decays of a chunk; arrays by row (token order). Steps are counted in
+// the order of time, which in reverse is from the last row.
+constexpr int kNoRestart = 255;
+struct Gates {
+  float hi[kChunk];              // c since the last restart: hi + lo
+  float near[kChunk];            // e^{c_r - c_j}, r: the last step of j's 32
+  float write[2][kChunk];        // sw e^{c_C - c_i}, 0 before a restart
+  unsigned short lo[kChunk];     // (bfloat16)
+  unsigned char from[kChunk];    // the last restart at or before the step
+  float keep[2];                 // e^{c_C}, 0 with a restart
+  int staged, dotted;            // what becomes of y (see the third group)
+  int dead;
+  uint32_t tmem;
+  uint64_t bars[kBars];
+};
+
+// The slots a chunk's weighted values come in: 8-step groups, the first step,
+// the buffer, its TMEM columns and those of one plane. Slot 0 and 4 are the
+// second warpgroup's, 1 the first's, 2 and 3 the third's.
+__host__ __device__ constexpr int slot_step(int s) {
+  return s < 3 ? s * 32 : s == 3 ? 80 : 112;
+}
+__host__ __device__ constexpr int slot_groups(int s) {
+  return s == 2 || s == 4 ? 2 : 4;
+}
+__host__ __device__ constexpr int slot_buffer(int s) {
+  return s == 1 ? 1 : s == 2 || s == 4 ? 2 : 0;
+}
+// How often the buffer has been filled before chunk `it` does it in slot s.
+__host__ __device__ constexpr int slot_use(int s, int it) {
+  return s == 1 ? it : 2 * it + (s >= 3);
+}
 
 template <int QD, int TV, int PS, bool STATE_ONLY>
 struct Lay {
@@ -150,238 +176,295 @@ __global__ void __launch_bounds__(kThreads, 1)
                     reinterpret_cast<const char *>(&gt));
   };
   auto bar = [&](int i) { return in_gates(&gt.bars[i]); };
-  volatile int *dead = &gt.dead;
   auto wait = [&](int i, int use) {
-    return tc::bar_wait(bar(i), uint32_t(use) & 1u, dead, pp.status);
+    return tc::bar_wait(bar(i), uint32_t(use) & 1u);
   };
   if (warp == 13) tc::tmem_alloc(in_gates(&gt.tmem), 512);
   if (threadIdx.x == 0) {
     gt.dead = 0;
-    for (int i = 0; i <= kFin; ++i)
-      tc::bar_init(bar(i), i >= kSingle && i < kFin ? 128 : 1);
+    gt.staged = !job.y_f32;
+    gt.dotted = job.rows != nullptr;
+#pragma unroll 1
+    for (int i = 0; i < kBars; ++i)
+      tc::bar_init(bar(i), i < kWeighed || i == kFin ? 1
+                           : i < kGatesFree          ? 128
+                           : i == kGatesFree         ? 256
+                                                     : 384);
     tc::fence_init();
   }
   tc::before_sync();
   __syncthreads();
   tc::after_sync();
-  const uint32_t tmem = gt.tmem;
+  // all of TMEM is this block's: it starts at column 0
+  constexpr uint32_t tmem = 0;
+  const bool fit = gt.tmem == tmem;
   const int64_t bh = b * p.heads + h;
   const int r = threadIdx.x % 128;  // a warpgroup's thread: its TMEM lane
   const uint32_t mine = tmem + (uint32_t(r / 32 * 32) << 16);
 
+  // The weighted values of one slot, this lane's value column, as three
+  // planes in the slot's buffer.
+  auto weigh = [&](int it, int slot) {
+    const int use = slot_use(slot, it), buf = slot_buffer(slot);
+    // A wait by parity has to come within one phase of its barrier. Where two
+    // slots take turns in a buffer, each warpgroup has waited for a later
+    // product of the chunk before; only the third one without outputs has
+    // not, and does it here.
+    if (STATE_ONLY && slot == 2 && it > 0 && !wait(kUpdate, it - 1))
+      return false;
+    if (use > 0 && !wait(kUsed + buf, use - 1)) return false;
+    if (r / 32 * 32 < TV) {
+      tc::after_sync();
+      const int t0 = slot_step(slot), groups = slot_groups(slot);
+      const unsigned char *col = smem + (it & 1) * L_::STAGE + L_::Q +
+                                 (r / 64) * 16384 + t0 * 128 + (r % 8) * 2;
+      const float *wt = gt.write[it & 1] + t0;
+      const int group = r % 64 / 8;
+      uint32_t dst = mine + L_::W + buf * 48;
+#pragma unroll 1
+      for (int g = 0; g < groups; ++g, col += 1024, wt += 8, dst += 4) {
+        uint32_t pl[3][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 w = *reinterpret_cast<const float2 *>(wt + 2 * i);
+          const uint32_t v0 = *reinterpret_cast<const uint16_t *>(
+              col + 2 * i * 128 + ((group ^ (2 * i % 8)) * 16));
+          const uint32_t v1 = *reinterpret_cast<const uint16_t *>(
+              col + (2 * i + 1) * 128 + ((group ^ ((2 * i + 1) % 8)) * 16));
+          float2 x = mul2(make_float2(__uint_as_float(v0 << 16),
+                                      __uint_as_float(v1 << 16)),
+                          w);
+#pragma unroll
+          for (int s = 0; s < 3; ++s) {
+            pl[s][i] = pack2(x.x, x.y);
+            if (s < 2)
+              x = fma2(make_float2(la::lo2(pl[s][i]), la::hi2(pl[s][i])),
+                       make_float2(-1.0f, -1.0f), x);
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < 3; ++s)
+          tc::tmem_st4(dst + s * groups * 4, pl[s]);
+      }
+      tc::tmem_wait_st();
+      tc::before_sync();
+    }
+    tc::bar_arrive(bar(kWeighed + slot));
+    return true;
+  };
+  // Whether chunk `it`'s values and weights are there.
+  auto chunk_in = [&](int it) {
+    return wait(kFull0 + (it & 1), it / 2) &&
+           wait(kWeights0 + (it & 1), it / 2);
+  };
+
   if (warp >= 12) {
+    // The code of a chunk's round, over all roles, has to stay within the SM's
+    // instruction cache (about 32 KB of it is hot here): warps that run alone
+    // wait for little else, so loops are rolled and nothing is inlined twice.
     if (warp == 12) {
       // ---- q, k, v in (stage it % 2), y out
       const int kh = h / (p.heads / job.k_heads);
       const int qh = h / (p.heads / job.q_heads);
       const int vh = h / (p.heads / job.v_heads);
-      auto load = [&](int it) {
-        if (lane == 0) {
-          const int st = it & 1, tok = low(it);
-          const uint32_t s = base + st * L_::STAGE, f = bar(kFull0 + st);
+      const bool staged = !STATE_ONLY && !job.y_f32;
+      int it = 0;
+#pragma unroll 1
+      for (; fit && it < n_live + 2; ++it) {
+        const int st = it & 1;
+        const uint32_t s = base + st * L_::STAGE, f = bar(kFull0 + st);
+        if (it >= 2) {
+          if (staged) {
+            if (!wait(kStaged, it - 2)) break;
+            if (lane == 0) {
+              const uint32_t y =
+                  L_::OVER_Q ? s + L_::Q + L_::V : base + L_::Y;
+#pragma unroll 1
+              for (int c = 0; c * 64 < job.vd; ++c)
+                tc::store_box(&maps[3], y + c * 16384, c * 64, h, low(it - 2),
+                              int(b));
+              tc::store_read();
+              tc::bar_arrive(bar(kStored));
+            }
+            __syncwarp();
+          }
+          if (it < n_live && !wait(kEmpty0 + st, it / 2 - 1)) break;
+        }
+        if (it < n_live && lane == 0) {
+          const int tok = low(it);
           tc::bar_expect(f, L_::STAGE);
+#pragma unroll 1
           for (int c = 0; c < QD / 64; ++c) {
             tc::load_box(s + c * 16384, &maps[1], f, c * 64, kh, tok, int(b));
             if (!STATE_ONLY)
               tc::load_box(s + L_::Q + L_::V + c * 16384, &maps[0], f, c * 64,
                            qh, tok, int(b));
           }
+#pragma unroll 1
           for (int c = 0; c < TV / 64; ++c)
             tc::load_box(s + L_::Q + c * 16384, &maps[2], f, c * 64, vh, tok,
                          int(b));
         }
         __syncwarp();
-      };
-      int loaded = 0;
-#pragma unroll 1
-      for (; loaded < n_live && loaded < 2; ++loaded) load(loaded);
-#pragma unroll 1
-      for (int it = 0; it < n_live; ++it) {
-        const int st = it & 1;
-        if (!STATE_ONLY && !job.y_f32) {
-          if (!wait(kStaged, it)) break;
-          if (lane == 0) {
-            const uint32_t y =
-                base + (L_::OVER_Q ? st * L_::STAGE + L_::Q + L_::V : L_::Y);
-#pragma unroll
-            for (int c = 0; c < TV / 64; ++c)
-              if (c * 64 < job.vd)
-              tc::store_box(&maps[3], y + c * 16384, c * 64, h,
-                            low(it), int(b));
-            tc::store_read();
-            tc::bar_arrive(bar(kStored));
-          }
-          __syncwarp();
-        }
-        if (it + 2 < n_live) {
-          if (!wait(kEmpty0 + st, it / 2)) break;
-          load(it + 2);
-          ++loaded;
-        }
       }
-      if (*dead)  // nothing may still be on its way into this block's memory
+      if (it < n_live + 2) {
+        // given up: nothing may still be on its way into this block's memory
+        gt.dead = 1;
+        const int loaded = it < n_live ? it : n_live;
 #pragma unroll 1
-        for (int it = loaded > 2 ? loaded - 2 : 0; it < loaded; ++it)
+        for (it = loaded > 2 ? loaded - 2 : 0; it < loaded; ++it)
 #pragma unroll 1
           for (int i = 0; i < 1 << 16; ++i)
             if (tc::bar_try(bar(kFull0 + (it & 1)), uint32_t(it / 2) & 1u))
               break;
+      }
     } else if (warp == 13) {
-      // ---- products, issued by one thread
-      if (lane == 0) {
-        constexpr uint32_t kScoreShape = tc::shape(128, false);
-        constexpr uint32_t kReadShape = tc::shape(TV, false);
-        constexpr uint32_t kUpdateShape = tc::shape(QD, true);
-        constexpr uint32_t kOutShape = tc::shape(TV, true);
-        // an operand's description for each step of 16 is the first one's
-        // plus the bytes between them (in units of 16)
-        const uint64_t stage0 = tc::operand(base, 16384);
-        const uint64_t state0 = tc::operand(base + L_::S, 0);
-        constexpr uint64_t kStage = L_::STAGE / 16, kV = L_::Q / 16,
-                           kQ = (L_::Q + L_::V) / 16;
-        auto one = [&](int i, int use) {
-          return tc::bar_wait_one(bar(i), uint32_t(use) & 1u, dead, pp.status);
-        };
-        // K-major: 64 steps to a 128-byte row, then `far` on
-        auto along = [](int ks, int far) {
-          return uint64_t((ks >> 2) * far + (ks & 3) * 2);
-        };
-        auto scores = [&](int it) {
-          const int st = it & 1;
-          const uint64_t K = stage0 + st * kStage, Q = K + kQ;
-          if (!one(kFull0 + st, it / 2)) return false;
-          if (it == ragged && !one(kClean, 0)) return false;
-          tc::after_sync();
-          if (!STATE_ONLY) {
-#pragma unroll
-            for (int ks = 0; ks < QD / 16; ++ks)
-              tc::mma_ss(tmem + L_::P, Q + along(ks, 1024),
-                         K + along(ks, 1024), kScoreShape, ks > 0);
-            tc::commit(bar(kScores));
-          }
-          return true;
-        };
-        bool alive = n_live > 0 && scores(0);
+      // ---- products, in a converged warp with uniform operands
+      constexpr uint32_t kScoreShape = tc::shape(128, false);
+      constexpr uint32_t kReadShape = tc::shape(TV, false);
+      constexpr uint32_t kUpdateShape = tc::shape(QD, true);
+      constexpr uint32_t kOutShape = tc::shape(TV, true);
+      const uint32_t e = tc::elected();
+      // an operand's description for each step of 16 is the first one's plus
+      // the bytes between them (in units of 16)
+      const uint64_t stage0 = tc::operand(base, 16384);
+      const uint64_t state0 = tc::operand(base + L_::S, 0);
+      constexpr uint64_t kStage = L_::STAGE / 16, kV = L_::Q / 16,
+                         kQ = (L_::Q + L_::V) / 16;
+      bool alive = fit;
+      // round i: chunk i - 1's update, reading and output, then chunk i's
+      // scores, which are decayed while the state is brought up to date
 #pragma unroll 1
-        for (int it = 0; it < n_live && alive; ++it) {
-          const int st = it & 1;
+      for (int i = 0; i <= n_live && alive; ++i) {
+        if (i > 0) {
+          const int it = i - 1, st = it & 1;
           const uint64_t K = stage0 + st * kStage, V = K + kV, Q = K + kQ;
-          alive = one(kState, it);
-          // the state's update first: the next chunk waits for it; what reads
-          // the state, and the scores' product, fill in behind
+          alive = wait(kState, it);
+          // the state's update first: the next chunk waits for it
 #pragma unroll 1
-          for (int qr = 0; qr < 4 && alive; ++qr) {
-            const int buf = qr & 1;
-            alive = one(kWFull0 + buf, it * 2 + qr / 2);
+          for (int slot = 0; slot < 5 && alive; ++slot) {
+            alive = wait(kWeighed + slot, it);
             if (!alive) break;
             tc::after_sync();
-            // planes from the smallest to the leading one, two steps of 16
-            const uint32_t w = tmem + L_::W + buf * 48;
-            const uint64_t k0 = K + uint64_t(qr * 256);
-#pragma unroll
-            for (int s = 2; s >= 0; --s) {
-              tc::mma_ts(tmem + L_::U, w + s * 16, k0, kUpdateShape,
-                         qr > 0 || s < 2);
-              tc::mma_ts(tmem + L_::U, w + s * 16 + 8, k0 + 128, kUpdateShape,
-                         true);
+            const int n = slot_groups(slot) / 2, buf = slot_buffer(slot);
+            uint32_t w = tmem + L_::W + buf * 48;
+            uint64_t k = K + uint64_t(slot_step(slot) * 8);
+#pragma unroll 1
+            for (int j = 0; j < n; ++j, w += 8, k += 128) {  // 16 steps
+              // planes from the smallest to the leading one
+              tc::mma_ts(e, tmem + L_::U, w + 16 * n, k, kUpdateShape,
+                         (slot | j) != 0);
+              tc::mma_ts(e, tmem + L_::U, w + 8 * n, k, kUpdateShape, true);
+              tc::mma_ts(e, tmem + L_::U, w, k, kUpdateShape, true);
             }
-            tc::commit(bar(kWEmpty0 + buf));
-            if (qr == 3) tc::commit(bar(kUpdate));
+            tc::commit(e, bar(kUsed + buf));
             if constexpr (!STATE_ONLY) {
-              if (qr == 0) {
-                alive = it == 0 || one(kOutRead, it - 1);
+              if (slot == 1) {
+                if (it > 0) alive = wait(kOutRead, it - 1);
                 if (!alive) break;
                 tc::after_sync();
+#pragma unroll 1
+                for (int s = PS - 1; s >= 0; --s)
 #pragma unroll
-                for (int i = 0; i < PS * QD / 16; ++i) {
-                  const int s = PS - 1 - i / (QD / 16), ks = i % (QD / 16);
-                  tc::mma_ss(tmem + L_::O, Q + along(ks, 1024),
-                             state0 + uint64_t(s * TV * QD / 8) +
-                                 along(ks, TV * 8),
-                             kReadShape, i > 0);
-                }
-                tc::commit(bar(kRead));
+                  for (int c = 0; c < QD / 64; ++c)
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                      tc::mma_ss(e, tmem + L_::O, Q + c * 1024 + ks * 2,
+                                 state0 + uint64_t(s * TV * QD / 8 +
+                                                   c * TV * 8 + ks * 2),
+                                 kReadShape, s < PS - 1 || c + ks > 0);
+                tc::commit(e, bar(kRead));
               }
             }
           }
           if (!alive) break;
+          tc::commit(e, bar(kUpdate));
           if constexpr (!STATE_ONLY) {
             // O2 is added to the scaled O1
-            alive = one(kScored, it) && one(kReadDone, it);
+            alive = wait(kScored, it) && wait(kReadDone, it);
             if (!alive) break;
             tc::after_sync();
+#pragma unroll 1
+            for (int s = PS - 1; s >= 0; --s)
 #pragma unroll
-            for (int i = 0; i < PS * 8; ++i) {
-              const int s = PS - 1 - i / 8, ks = i % 8;
-              tc::mma_ts(tmem + L_::O,
-                         tmem + L_::P + (ks / 2) * 32 + s * 16 + (ks % 2) * 8,
-                         V + uint64_t(ks * 128), kOutShape, true);
-            }
-            tc::commit(bar(kOut));
+              for (int ks = 0; ks < 8; ++ks)
+                tc::mma_ts(e, tmem + L_::O, tmem + L_::P + ks * 16 + s * 8,
+                           V + uint64_t(ks * 128), kOutShape, true);
+            tc::commit(e, bar(kOut));
           }
-          tc::commit(bar(kEmpty0 + st));
-          if (it + 1 < n_live) alive = scores(it + 1);
+          tc::commit(e, bar(kEmpty0 + st));
+        }
+        if (i < n_live) {
+          const int st = i & 1;
+          const uint64_t K = stage0 + st * kStage, Q = K + kQ;
+          alive = wait(kFull0 + st, i / 2) && (i != ragged || wait(kClean, 0));
+          if (!alive) break;
+          tc::after_sync();
+          if constexpr (!STATE_ONLY) {
+            // K-major: 64 steps to a 128-byte row
+#pragma unroll
+            for (int c = 0; c < QD / 64; ++c)
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                tc::mma_ss(e, tmem + L_::P, Q + c * 1024 + ks * 2,
+                           K + c * 1024 + ks * 2, kScoreShape, c + ks > 0);
+            tc::commit(e, bar(kScores));
+          }
         }
       }
-      __syncwarp();
+      if (!alive) gt.dead = 1;
       // every product is done before the block goes
-      if (lane == 0) tc::commit(bar(kFin));
-      __syncwarp();
+      tc::commit(e, bar(kFin));
 #pragma unroll 1
       for (int i = 0; i < 1 << 16; ++i)
         if (tc::bar_try(bar(kFin), 0)) break;
+      __syncwarp();
     } else {
       // ---- decays: every second chunk each, four steps a lane in the order
       // of time; the next values are on their way while these are summed
-      const bf16 *gate = static_cast<const bf16 *>(p.log_decay);
+      const unsigned short *gate =
+          p.log_decay ? static_cast<const unsigned short *>(p.log_decay) +
+                            b * L * p.heads + h
+                      : nullptr;
       const double head = p.head_log_decay ? p.head_log_decay[h] : 0.0;
-      unsigned short raw[4];
+      unsigned short raw[4] = {0, 0, 0, 0};
+      auto token = [&](int it, int j) {
+        const int s = 4 * lane + j;
+        return rev ? low(it) + kChunk - s : low(it) + s;
+      };
       auto fetch = [&](int it) {
-        const int lo = low(it);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int s = 4 * lane + j;
-          const int64_t t = rev ? lo + kChunk - s : lo + s;
-          raw[j] = 0;
-          if (gate && t < len)
-            raw[j] = __ldg(reinterpret_cast<const unsigned short *>(gate) +
-                           (b * L + t) * p.heads + h);
+          const int t = token(it, j);
+          if (gate && t < len) raw[j] = __ldg(gate + int64_t(t) * p.heads);
         }
       };
-      // The last chunk's values have been written (by the other warp) and
-      // used. Without the first wait the second could run a phase ahead of
-      // its barrier and pass on the parity of an old one.
-      auto turn = [&](int written, int used, int it) {
-        return it == 0 || (wait(written, it - 1) && wait(used, it - 1));
-      };
-      if (warp - 14 < n_live) fetch(warp - 14);
+      // round -1 only reads
+      bool alive = true;
 #pragma unroll 1
-      for (int it = warp - 14; it < n_live; it += 2) {
+      for (int it = warp - 16; it < n_live && alive; it += 2) {
         double c[4], sum = 0.0;
         int from[4], lastr = -1;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int lo = low(it);
-          const int s = 4 * lane + j;
-          const int64_t t = rev ? lo + kChunk - s : lo + s;
           const double g =
-              t < len ? (double(__uint_as_float(uint32_t(raw[j]) << 16)) +
-                         head) *
-                            1.4426950408889634
-                      : 0.0;
+              it >= 0 && token(it, j) < len
+                  ? (double(__uint_as_float(uint32_t(raw[j]) << 16)) + head) *
+                        1.4426950408889634
+                  : 0.0;
+          sum += g;
           if (g < -126.0) {
             sum = 0.0;
-            lastr = s;
-          } else {
-            sum += g;
+            lastr = 4 * lane + j;
           }
           c[j] = sum;
           from[j] = lastr;
         }
         if (it + 2 < n_live) fetch(it + 2);
+        if (it < 0) continue;
         double ps = sum;
         int pr = lastr;
-#pragma unroll
+#pragma unroll 1
         for (int d = 1; d < 32; d <<= 1) {
           const double os = __shfl_up_sync(0xffffffffu, ps, d);
           const int orr = __shfl_up_sync(0xffffffffu, pr, d);
@@ -400,49 +483,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int end_r = __shfl_sync(0xffffffffu, pr, 31);
         const double blk = __shfl_sync(0xffffffffu, ps, lane | 7);
         const int blk_r = __shfl_sync(0xffffffffu, pr, lane | 7);
-        float hi[4], lo4[4], near[4], read[4], write[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int s = 4 * lane + j;
+        for (int j = 0; j < 4; ++j)
           if (from[j] < 0) {
             c[j] += es;
             from[j] = er;
           }
-          hi[j] = float(c[j]);
-          lo4[j] = float(c[j] - double(hi[j]));
-          near[j] = s >= blk_r ? ex2_d(blk - c[j]) : 0.0f;
-          read[j] = from[j] < 0 ? ex2_d(c[j]) * job.si : 0.0f;
-          write[j] = s >= end_r ? ex2_d(end - c[j]) * job.sw : 0.0f;
-          from[j] = from[j] < 0 ? 0 : from[j];
-        }
-        const float keep = end_r < 0 ? ex2_d(end) : 0.0f;
-        // in reverse, a lane's four steps are its four rows backwards
-        const int row = rev ? kChunk - 4 - 4 * lane : 4 * lane;
-        auto put = [&](float *dst, const float (&v)[4]) {
-          *reinterpret_cast<float4 *>(dst + row) =
-              rev ? make_float4(v[3], v[2], v[1], v[0])
-                  : make_float4(v[0], v[1], v[2], v[3]);
+        auto pick = [](int j, const auto (&v)[4]) {
+          return j & 2 ? (j & 1 ? v[3] : v[2]) : (j & 1 ? v[1] : v[0]);
         };
-        if (!STATE_ONLY) {
-          if (!turn(kGatesA, kFreeA, it)) break;
-          put(gt.hi, hi);
-          put(gt.lo, lo4);
-          put(gt.near, near);
-          *reinterpret_cast<uchar4 *>(gt.from + row) =
-              rev ? make_uchar4(from[3], from[2], from[1], from[0])
-                  : make_uchar4(from[0], from[1], from[2], from[3]);
-          __syncwarp();
-          if (lane == 0) tc::bar_arrive(bar(kGatesA));
-          if (!turn(kGatesC, kFreeC, it)) break;
-          put(gt.read, read);
-          __syncwarp();
-          if (lane == 0) tc::bar_arrive(bar(kGatesC));
+        // (a weight e^-x is off by x e^-x 2^-24 at most for the rounding of
+        // x); this warp's own last weights have been used
+        const int par = it & 1;
+        if (it >= 2) alive = wait(kWeightsFree0 + par, it / 2 - 1);
+        if (!alive) break;
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          const int s = 4 * lane + j, row = rev ? kChunk - 1 - s : s;
+          gt.write[par][row] =
+              s >= end_r ? ex2(float(end - pick(j, c))) * job.sw : 0.0f;
         }
-        if (!turn(kGatesB, kFreeB, it)) break;
-        put(gt.write, write);
-        if (lane == 0) gt.keep = keep;
+        if (lane == 0) gt.keep[par] = end_r < 0 ? ex2(float(end)) : 0.0f;
         __syncwarp();
-        if (lane == 0) tc::bar_arrive(bar(kGatesB));
+        if (lane == 0) tc::bar_arrive(bar(kWeights0 + par));
+        if constexpr (!STATE_ONLY) {
+          // the last chunk's values have been written (by the other warp) and
+          // used; without the first wait this one could run a phase ahead of
+          // its barrier and pass on the parity of an old one
+          if (it > 0) alive = wait(kGates, it - 1) && wait(kGatesFree, it - 1);
+          if (!alive) break;
+#pragma unroll 1
+          for (int j = 0; j < 4; ++j) {
+            const int s = 4 * lane + j, row = rev ? kChunk - 1 - s : s;
+            const double cj = pick(j, c);
+            const int fj = pick(j, from);
+            const float hi = float(cj);
+            gt.hi[row] = hi;
+            gt.lo[row] =
+                (unsigned short)pack2(float(cj - double(hi)), 0.0f);
+            gt.near[row] = s >= blk_r ? ex2(float(blk - cj)) : 0.0f;
+            gt.from[row] = (unsigned char)(fj < 0 ? kNoRestart : fj);
+          }
+          __syncwarp();
+          if (lane == 0) tc::bar_arrive(bar(kGates));
+        }
       }
     }
   } else if (warp < 4) {
@@ -452,82 +536,93 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int step = rev ? kChunk - 1 - r : r;
     const int tb = rev ? 3 - warp : warp;
 #pragma unroll 1
-    for (int it = 0; !STATE_ONLY && it < n_live; ++it) {
-      if (!wait(kGatesA, it) || !wait(kScores, it)) break;
+    for (int it = 0; it < n_live; ++it) {
+      if (!chunk_in(it) || (it == ragged && !wait(kClean, 0)) ||
+          !weigh(it, 1))
+        break;
+      tc::bar_arrive(bar(kWeightsFree0 + (it & 1)));
+      if constexpr (STATE_ONLY) continue;
+      if (!wait(kGates, it) || !wait(kScores, it)) break;
       tc::after_sync();
-      const int from = gt.from[r];
-      const float chi = gt.hi[r], clo = gt.lo[r];
+      const int rs = gt.from[r], from = rs == kNoRestart ? 0 : rs;
+      const float chi = gt.hi[r],
+                  clo = __uint_as_float(uint32_t(gt.lo[r]) << 16);
+      float e = 0.0f;
 #pragma unroll 1
-      for (int nb = 0; nb < 4; ++nb) {     // blocks of 32 rows j
-        const int jb = rev ? 3 - nb : nb;  // in time
-        uint32_t v[32], late[PS == 2 ? 16 : 1];
-        if (jb > tb) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0u;
-        } else {
-          tc::tmem_ld32(mine + L_::P + nb * 32, v);
+      for (int sb = 0; sb < 8; ++sb) {     // 16 rows j
+        const int nb = sb / 2, jb = rev ? 3 - nb : nb;  // their 32; in time
+        uint32_t v[16];
+        if (jb <= tb) {
+          tc::tmem_ld16(mine + L_::P + sb * 16, v);
           tc::tmem_wait_ld();
-          if (jb < tb) {
-            const int ref = rev ? nb * 32 : nb * 32 + 31;  // row of step r
-            float e = 0.0f;
-            if (from <= jb * 32 + 31)
-              e = ex2((chi - gt.hi[ref]) + (clo - gt.lo[ref])) * job.sp;
+        }
+        if (jb < tb) {
+          const int ref = rev ? nb * 32 : nb * 32 + 31;  // row of step r
+          e = from <= jb * 32 + 31
+                  ? ex2((chi - gt.hi[ref]) +
+                        (clo - __uint_as_float(uint32_t(gt.lo[ref]) << 16))) *
+                        job.sp
+                  : 0.0f;
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 f =
-                  *reinterpret_cast<const float4 *>(gt.near + nb * 32 + i);
-              const float d[4] = {f.x, f.y, f.z, f.w};
+          for (int i = 0; i < 16; i += 4) {
+            const float4 f =
+                *reinterpret_cast<const float4 *>(gt.near + sb * 16 + i);
+            const float d[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                v[i + j] =
-                    __float_as_uint(__uint_as_float(v[i + j]) * (e * d[j]));
-            }
-          } else {
-            // rows of steps in [from, step] of this block, as bits
-            const int lo_s = max(from - jb * 32, 0), hi_s = step - jb * 32;
-            uint32_t keep_bits = (0xffffffffu >> (31 - hi_s)) &
-                                 (0xffffffffu << lo_s);
-            if (rev) keep_bits = __brev(keep_bits);
+            for (int j = 0; j < 4; ++j)
+              v[i + j] =
+                  __float_as_uint(__uint_as_float(v[i + j]) * (e * d[j]));
+          }
+        } else if (jb == tb) {
+          // rows of steps in [from, step] of this block of 32, as bits
+          const int lo_s = max(from - jb * 32, 0), hi_s = step - jb * 32;
+          uint32_t bits =
+              (0xffffffffu >> (31 - hi_s)) & (0xffffffffu << lo_s);
+          if (rev) bits = __brev(bits);
+          bits >>= (sb & 1) * 16;
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 fh =
-                  *reinterpret_cast<const float4 *>(gt.hi + nb * 32 + i);
-              const float4 fl =
-                  *reinterpret_cast<const float4 *>(gt.lo + nb * 32 + i);
-              const float dh[4] = {fh.x, fh.y, fh.z, fh.w};
-              const float dl[4] = {fl.x, fl.y, fl.z, fl.w};
+          for (int i = 0; i < 16; i += 4) {
+            const float4 fh =
+                *reinterpret_cast<const float4 *>(gt.hi + sb * 16 + i);
+            const uint2 fl =
+                *reinterpret_cast<const uint2 *>(gt.lo + sb * 16 + i);
+            const float dh[4] = {fh.x, fh.y, fh.z, fh.w};
+            const float dl[4] = {la::lo2(fl.x), la::hi2(fl.x), la::lo2(fl.y),
+                                 la::hi2(fl.y)};
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float d = ex2((chi - dh[j]) + (clo - dl[j])) * job.sp;
-                v[i + j] =
-                    keep_bits >> (i + j) & 1u
-                        ? __float_as_uint(__uint_as_float(v[i + j]) * d)
-                        : 0u;
-              }
+            for (int j = 0; j < 4; ++j) {
+              const float d = ex2((chi - dh[j]) + (clo - dl[j])) * job.sp;
+              v[i + j] = bits >> (i + j) & 1u
+                             ? __float_as_uint(__uint_as_float(v[i + j]) * d)
+                             : 0u;
             }
           }
-        }
-        // P' takes the place of its block of P: 16 columns a plane
+        } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < 16; ++i) v[i] = 0u;
+        }
+        // P' takes the place of its 16 columns of P: 8 a plane
+        uint32_t w[PS][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
           uint32_t pl[PS];
           la::split2<PS>(__uint_as_float(v[2 * i]),
                          __uint_as_float(v[2 * i + 1]), pl);
-          v[i] = pl[0];
-          if constexpr (PS == 2) late[i] = pl[1];
+#pragma unroll
+          for (int s = 0; s < PS; ++s) w[s][i] = pl[s];
         }
-        tc::tmem_st16(mine + L_::P + nb * 32, v);
-        if constexpr (PS == 2) tc::tmem_st16(mine + L_::P + nb * 32 + 16, late);
+#pragma unroll
+        for (int s = 0; s < PS; ++s)
+          tc::tmem_st8(mine + L_::P + sb * 16 + s * 8, w[s]);
       }
       tc::tmem_wait_st();
-      tc::bar_arrive(bar(kFreeA));
+      tc::bar_arrive(bar(kGatesFree));
       tc::before_sync();
       tc::bar_arrive(bar(kScored));
     }
   } else if (warp < 8) {
     // ---- the weighted values and the state; lane: a value column
     tc::more_registers<208>();
-    const bool has_v = r / 32 * 32 < TV;
     constexpr int64_t SF = int64_t(QD) * kLaTile;
     const int tiles = (job.vd + kLaTile - 1) / kLaTile;
     // element (key, value r) of a segment's state
@@ -538,20 +633,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                   r % kLaTile
             : nullptr;
     float S[QD];
+    {
+      const float *src = nullptr;
+      int keys = 0;
+      int64_t stride = kLaTile;
+      if (!STATE_ONLY && p.nseg > 1) {
+        src = seg_state;
+        keys = QD;
+      } else if (!STATE_ONLY && job.init && r < job.vd) {
+        src = job.init + bh * job.qd * job.vd + int64_t(r) * job.state_cs;
+        keys = job.qd;
+        stride = job.state_rs;
+      }
+      if (!src) keys = 0;
 #pragma unroll
-    for (int i = 0; i < QD; ++i) S[i] = 0.0f;
-    if (!STATE_ONLY && r < TV) {
-      if (p.nseg > 1) {
-        if (seg_state) {
-#pragma unroll
-          for (int i = 0; i < QD; ++i) S[i] = seg_state[i * kLaTile];
-        }
-      } else if (job.init && r < job.vd) {
-        const float *src =
-            job.init + bh * job.qd * job.vd + int64_t(r) * job.state_cs;
-#pragma unroll
-        for (int i = 0; i < QD; ++i)
-          if (i < job.qd) S[i] = src[int64_t(i) * job.state_rs];
+      for (int i = 0; i < QD; ++i) {
+        S[i] = i < keys ? *src : 0.0f;
+        src += stride;
       }
     }
     // the bfloat16 planes of the state
@@ -577,98 +675,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::before_sync();
       tc::bar_arrive(bar(kState));
     };
-    float keep = 0.0f, next_keep = 0.0f, seg_keep = 1.0f;
-    // a chunk's values are there, zeros behind the sequence's end
-    auto begin = [&](int it) {
-      const int st = it & 1;
-      if (!wait(kFull0 + st, it / 2) || !wait(kGatesB, it)) return false;
-      if (it == ragged) {
-        // whatever was loaded
-        unsigned char *Ks = smem + st * L_::STAGE, *Vs = Ks + L_::Q;
-        const int dead_from = int(len - low(it));
-#pragma unroll 1
-        for (int i = r + dead_from * 8; i < kChunk * 8; i += 128) {
-#pragma unroll
-          for (int c = 0; c < QD / 64; ++c)
-            *reinterpret_cast<uint4 *>(Ks + c * 16384 + i * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int c = 0; c < TV / 64; ++c)
-            *reinterpret_cast<uint4 *>(Vs + c * 16384 + i * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-        }
-        tc::fence_async();
-        tc::bar_arrive(bar(kClean));
-        if (!wait(kClean, 0)) return false;
-      }
-      next_keep = gt.keep;
-      return true;
-    };
-    // weighted values of 32 steps, this lane's column
-    auto weigh = [&](int it, int qr) {
-      const int buf = qr & 1, use = it * 2 + qr / 2;
-      if (use > 0 && !wait(kWEmpty0 + buf, use - 1)) return false;
-      tc::after_sync();
-      if (has_v) {
-        const unsigned char *col = smem + (it & 1) * L_::STAGE + L_::Q +
-                                   (r / 64) * 16384 + qr * 4096 + (r % 8) * 2;
-        const float *wt = gt.write + qr * 32;
-        const int group = r % 64 / 8;
-        uint32_t pl[3][16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 w = *reinterpret_cast<const float2 *>(wt + 2 * i);
-          const float v0 = __uint_as_float(
-              uint32_t(*reinterpret_cast<const uint16_t *>(
-                  col + 2 * i * 128 + ((group ^ ((2 * i) % 8)) * 16)))
-              << 16);
-          const float v1 = __uint_as_float(
-              uint32_t(*reinterpret_cast<const uint16_t *>(
-                  col + (2 * i + 1) * 128 +
-                  ((group ^ ((2 * i + 1) % 8)) * 16)))
-              << 16);
-          uint32_t s3[3];
-          la::split2<3>(v0 * w.x, v1 * w.y, s3);
-#pragma unroll
-          for (int s = 0; s < 3; ++s) pl[s][i] = s3[s];
-        }
-#pragma unroll
-        for (int s = 0; s < 3; ++s)
-          tc::tmem_st16(mine + L_::W + buf * 48 + s * 16, pl[s]);
-        tc::tmem_wait_st();
-      }
-      tc::before_sync();
-      tc::bar_arrive(bar(kWFull0 + buf));
-      return true;
-    };
+    float seg_keep = 1.0f;
     put_state();
-    // The first quarter of a chunk's values is weighed before the last
-    // chunk's update is waited for: there is a buffer free for it, and the
-    // products of the last quarter are still under way.
-    bool alive = n_live == 0 || begin(0);
+    // In turn: the first slot of chunk it, the update by chunk it - 1 (whose
+    // products are under way meanwhile), the last slot of chunk it.
+    bool alive = fit;
 #pragma unroll 1
-    for (int i = 0; i < 4 * n_live && alive; ++i) {
-      const int it = i / 4;
-      alive = weigh(it, i % 4);
-      if (!alive) break;
-      if (i % 4 == 0) {
-        if (it == 0) {
-          keep = next_keep;
-          seg_keep *= keep;
-          continue;
+    for (int i = 0; alive && i < 2 * n_live + 1; ++i) {
+      const int it = i / 2, st = it & 1;
+      if (it < n_live) {
+        if (i % 2 == 0) {
+          alive = chunk_in(it);
+          if (alive && it == ragged) {
+            // rows behind the sequence's end: zeros, whatever was loaded
+            unsigned char *Ks = smem + st * L_::STAGE, *Vs = Ks + L_::Q;
+            const int dead_from = int(len - low(it));
+#pragma unroll 1
+            for (int z = r + dead_from * 8; z < kChunk * 8; z += 128) {
+#pragma unroll
+              for (int c = 0; c < QD / 64; ++c)
+                *reinterpret_cast<uint4 *>(Ks + c * 16384 + z * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+              for (int c = 0; c < TV / 64; ++c)
+                *reinterpret_cast<uint4 *>(Vs + c * 16384 + z * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+            tc::fence_async();
+            tc::bar_arrive(bar(kClean));
+            alive = wait(kClean, 0);
+          }
         }
-      } else if (i % 4 < 3) {
-        continue;
-      } else {
-        tc::bar_arrive(bar(kFreeB));
-        if (it + 1 < n_live) {
-          alive = begin(it + 1);
-          continue;
-        }
+        alive = alive && weigh(it, i % 2 == 0 ? 0 : 4);
+        if (!alive) break;
       }
-      // here after the first quarter of every chunk but the first, and at the
-      // very end: the update of the chunk before
-      const int done = i % 4 == 0 ? it - 1 : it;
+      if (i % 2 == 1 || it == 0) continue;
+      const int done = it - 1;
+      const float keep = gt.keep[done & 1];
+      seg_keep *= keep;
+      tc::bar_arrive(bar(kWeightsFree0 + (done & 1)));
       alive = wait(kUpdate, done);
       if (!alive) break;
       tc::after_sync();
@@ -686,36 +731,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           S[u + i] = fmaf(keep, S[u + i], __uint_as_float(t[i]));
       }
       put_state();
-      keep = next_keep;
-      if (done + 1 < n_live) seg_keep *= keep;
     }
-    if (alive && r < TV) {
-      if constexpr (STATE_ONLY) {
-        if (seg_state) {
+    if (!alive) gt.dead = 1;
+    float *dst = nullptr;
+    int keys = 0;
+    int64_t stride = kLaTile;
+    if (STATE_ONLY) {
+      dst = seg_state;
+      keys = QD;
+      if (r == 0) job.seg_decay[bh * p.nseg + seg] = seg_keep;
+    } else if (job.last && seg == p.nseg - 1 && r < job.vd) {
+      dst = job.last + bh * job.qd * job.vd + int64_t(r) * job.state_cs;
+      keys = job.qd;
+      stride = job.state_rs;
+      // running backwards, the first token's own decay is still to come
+      if (rev && len > 0) {
+        const float f =
+            ex2_d(la::gate_at<bf16>(p, b, 0, h) * 1.4426950408889634);
 #pragma unroll
-          for (int i = 0; i < QD; ++i) seg_state[i * kLaTile] = S[i];
-        }
-        if (r == 0) job.seg_decay[bh * p.nseg + seg] = seg_keep;
-      } else if (job.last && seg == p.nseg - 1 && r < job.vd) {
-        // running backwards, the first token's own decay is still to come
-        float f = 1.0f;
-        if (rev && len > 0)
-          f = ex2_d(la::gate_at<bf16>(p, b, 0, h) * 1.4426950408889634);
-        float *dst =
-            job.last + bh * job.qd * job.vd + int64_t(r) * job.state_cs;
-#pragma unroll
-        for (int i = 0; i < QD; ++i)
-          if (i < job.qd)
-            dst[int64_t(i) * job.state_rs] = f == 0.0f ? 0.0f : S[i] * f;
+        for (int i = 0; i < QD; ++i) S[i] = f == 0.0f ? 0.0f : S[i] * f;
       }
+    }
+    if (!alive || !dst) keys = 0;
+#pragma unroll
+    for (int i = 0; i < QD; ++i) {
+      if (i < keys) *dst = S[i];
+      dst += stride;
     }
   } else {
     // ---- y; lane: a step
     tc::fewer_registers<88>();
-    if constexpr (!STATE_ONLY) {
+    {
       // rows of y behind the sequence's last live chunk
 #pragma unroll 1
-      for (int64_t t = idle_low + r; t < seg_low + p.seg_len && t < L;
+      for (int64_t t = STATE_ONLY ? L : idle_low + r; t < seg_low + p.seg_len && t < L;
            t += 128) {
         const int64_t at = ((b * L + t) * p.heads + h) * job.vd;
         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
@@ -734,10 +783,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int it = 0; it < n_live; ++it) {
         const int st = it & 1;
+        if (!chunk_in(it) || (it == ragged && !wait(kClean, 0))) break;
+        bool alive = true;
+#pragma unroll 1
+        for (int slot = 2; slot < 4 && alive; ++slot) alive = weigh(it, slot);
+        if (!alive) break;
+        tc::bar_arrive(bar(kWeightsFree0 + st));
+        if constexpr (STATE_ONLY) continue;
         // O1, scaled in its place: O2 is added to it there
-        if (!wait(kGatesC, it) || !wait(kRead, it)) break;
+        if (!wait(kGates, it) || !wait(kRead, it)) break;
         tc::after_sync();
-        const float rd = gt.read[r];
+        const float rd =
+            gt.from[r] == kNoRestart ? ex2(gt.hi[r]) * job.si : 0.0f;
 #pragma unroll 1
         for (int u = 0; u < TV; u += 32) {
           uint32_t v[32];
@@ -752,24 +809,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tmem_st16(mine + L_::O + u + 16, v + 16);
         }
         tc::tmem_wait_st();
-        tc::bar_arrive(bar(kFreeC));
+        tc::bar_arrive(bar(kGatesFree));
         tc::before_sync();
         tc::bar_arrive(bar(kReadDone));
         const int64_t t = low(it) + r;
         const bool live = t < len;
         const bool staged = !job.y_f32;
-        if (staged && !L_::OVER_Q && it > 0 && !wait(kStored, it - 1)) break;
+        if (staged && it > 0 && !wait(kStored, it - 1)) break;
         if (!wait(kOut, it)) break;
         tc::after_sync();
         unsigned char *ys =
             smem + (L_::OVER_Q ? st * L_::STAGE + L_::Q + L_::V : L_::Y);
         const int64_t row = (b * L + t) * p.heads + h;
-        const bf16 *ds =
-            job.rows ? static_cast<const bf16 *>(job.dot) +
-                           (b * L + t) * job.dot_stride +
-                           int64_t(h / (p.heads / job.dot_heads)) * job.vd
-                     : nullptr;
         float dot = 0.0f;
+        // (the flags are read in the loop, so that it stays one loop)
+        volatile const int *is_staged = &gt.staged, *is_dotted = &gt.dotted;
 #pragma unroll 1
         for (int u = 0; u < TV; u += 32) {
           uint32_t v[32];
@@ -779,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0u;
           }
-          if (staged) {
+          if (*is_staged) {
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
               uint32_t w[4];
@@ -800,8 +854,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4 *>(y + i) =
                     make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
           }
-          if (ds && live) {
+          if (*is_dotted && live) {
             // the row dots the decay's gradient is made of
+            const bf16 *ds = static_cast<const bf16 *>(job.dot) +
+                             (b * L + t) * job.dot_stride +
+                             int64_t(h / (p.heads / job.dot_heads)) * job.vd;
 #pragma unroll
             for (int i = 0; i < 32; i += 8)
               if (u + i < job.vd) {
@@ -831,7 +888,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::before_sync();
   __syncthreads();
   tc::after_sync();
-  if (warp == 13) tc::tmem_free(tmem, 512);
+  if (warp == 13) tc::tmem_free(gt.tmem, 512);
+  if (threadIdx.x == 0 && gt.dead) *pp.status = 1;
 }
 
 }  // namespace lat

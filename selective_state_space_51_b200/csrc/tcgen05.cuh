@@ -41,33 +41,24 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 }
 
 // Waits are bounded: a barrier that does not come within about a second ends
-// the block's work (`dead`, seen by every other wait) and is reported through
-// the device's status word.
+// the block's work, role by role, and is reported through the device's status
+// word. The whole warp waits and has one answer.
 constexpr unsigned kPolls = 1000u * 1000u;
 
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity,
-                                         volatile int *dead, int *status) {
-#pragma unroll 1
-  for (unsigned i = 0; i < kPolls; ++i) {
-    if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
-    if (*dead) return false;
-  }
-  *dead = 1;
-  *status = 1;
-  return false;
-}
-
-// The same for one thread on its own.
-__device__ __forceinline__ bool bar_wait_one(uint32_t bar, uint32_t parity,
-                                             volatile int *dead, int *status) {
-#pragma unroll 1
-  for (unsigned i = 0; i < kPolls; ++i) {
-    if (bar_try(bar, parity)) return true;
-    if (*dead) return false;
-  }
-  *dead = 1;
-  *status = 1;
-  return false;
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b32 n;\n"
+      " mov.b32 n, %3;\n"
+      "WAIT_%=:\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n"
+      " @p bra DONE_%=;\n"
+      " add.u32 n, n, -1;\n setp.ne.u32 q, n, 0;\n @q bra WAIT_%=;\n"
+      "DONE_%=:\n selp.b32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "n"(kPolls)
+      : "memory");
+  return __all_sync(0xffffffffu, ok);
 }
 
 // ---- proxies and TMEM ordering
@@ -99,7 +90,17 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
                "r"(cols));
 }
 
-// 32 columns of this thread's lane.
+// 16, 32 columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
+        "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15])
+      : "r"(addr));
+}
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -134,6 +135,12 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t *r) {
       "r"(r[6]), "r"(r[7])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st4(uint32_t addr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -155,29 +162,45 @@ __host__ __device__ constexpr uint32_t shape(int n, bool b_across) {
          uint32_t(n / 8) << 17 | uint32_t(128 / 16) << 24;
 }
 
+// One thread of a converged warp: what follows takes this flag, so that the
+// warp's control flow and its operands stay uniform.
+__device__ __forceinline__ uint32_t elected() {
+  uint32_t e;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n"
+      " selp.b32 %0, 1, 0, p;\n}"
+      : "=r"(e));
+  return e;
+}
+
 // D[128][n] (+)= A[128][16] B[16][n]; A from shared memory or from TMEM (lane:
 // row, column: a pair of steps).
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b,
-                                       uint32_t desc, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t e, uint32_t d, uint64_t a,
+                                       uint64_t b, uint32_t desc, bool add) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(desc), "r"(uint32_t(add))
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n"
+      " setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(desc), "r"(uint32_t(add)), "r"(e)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b,
-                                       uint32_t desc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t e, uint32_t d, uint32_t a,
+                                       uint64_t b, uint32_t desc, bool add) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(desc), "r"(uint32_t(add))
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n"
+      " setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(
+          d),
+      "r"(a), "l"(b), "r"(desc), "r"(uint32_t(add)), "r"(e)
       : "memory");
 }
 // Arrives once every product issued so far is done.
-__device__ __forceinline__ void commit(uint32_t bar) {
+__device__ __forceinline__ void commit(uint32_t e, uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 "
-      "[%0];" ::"r"(bar)
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster"
+      ".b64 [%0];\n}" ::"r"(bar),
+      "r"(e)
       : "memory");
 }
 
@@ -191,7 +214,6 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map,
       "l"(map), "r"(bar), "r"(x), "r"(head), "r"(token), "r"(batch)
       : "memory");
 }
-
 __device__ __forceinline__ void store_box(const CUtensorMap *map, uint32_t src,
                                           int x, int head, int token,
                                           int batch) {
