@@ -18,12 +18,16 @@
 // steps, which all need the same arithmetic, and have one task of their own
 // each: the first turns P into P', the second holds the state, the third
 // scales O1 in its place (O2 is added to it there) and hands y to a TMA store.
-// The weighted values pass through three buffers of 32, 32 and 16 steps, so
-// that the first 80 steps of a chunk are ready while the state of the last one
-// is still being added up. Of the fourth warpgroup, warp 12 moves q, k, v (two
-// chunks deep) and y, 13 issues the products, 14 and 15 sum the decays ahead
-// of their chunks. Everything between them goes through mbarriers with bounded
-// waits; the registers are divided by need.
+// The weighted values pass through three buffers of 32, 32 and 16 steps: the
+// first and the third group have theirs ready while the last chunk's state is
+// still being added up, the second follows once it is. Of the fourth
+// warpgroup, warp 12 moves q, k, v (two chunks deep) and y, 13 issues the
+// products, 14 and 15 sum the decays ahead of their chunks. Everything between
+// them goes through mbarriers with bounded waits; the registers are divided by
+// need.
+//
+// A wait by parity has to come within one phase of its barrier: every wait
+// here is for a phase that cannot be followed by the next before it returns.
 //
 // The decay e^{c_i - c_j}: outside the 32 x 32 blocks on the diagonal it is
 // e^{c_i - c_r} e^{c_r - c_j}, r the last step of j's block: both factors are
@@ -53,7 +57,7 @@ enum Bar {
   kRead,               // O1
   kOut,                // O2
   kUpdate,             // U
-  kUsed,               // (3) a buffer of weighted values has been used
+  kUsed,               // (3) slots 0, 1, 2 of weighted values have been used
   kGates = kUsed + 3,  // hi, lo, near, from
   kWeights0, kWeights1,  // write, keep of every second chunk
   kStored,             // y has been read by its store
@@ -87,22 +91,16 @@ struct Gates {
   uint64_t bars[kBars];
 };
 
-// The slots a chunk's weighted values come in: 8-step groups, the first step,
-// the buffer, its TMEM columns and those of one plane. Slot 0 and 4 are the
-// second warpgroup's, 1 the first's, 2 and 3 the third's.
+// The slots a chunk's weighted values come in: the first step, 8-step groups,
+// the buffer. Slot 0 is the first warpgroup's, 1 the third's, the others the
+// second's.
 __host__ __device__ constexpr int slot_step(int s) {
   return s < 3 ? s * 32 : s == 3 ? 80 : 112;
 }
 __host__ __device__ constexpr int slot_groups(int s) {
   return s == 2 || s == 4 ? 2 : 4;
 }
-__host__ __device__ constexpr int slot_buffer(int s) {
-  return s == 1 ? 1 : s == 2 || s == 4 ? 2 : 0;
-}
-// How often the buffer has been filled before chunk `it` does it in slot s.
-__host__ __device__ constexpr int slot_use(int s, int it) {
-  return s == 1 ? it : 2 * it + (s >= 3);
-}
+__host__ __device__ constexpr int slot_buffer(int s) { return s < 3 ? s : s == 3 ? 0 : 2; }
 
 template <int QD, int TV, int PS, bool STATE_ONLY>
 struct Lay {
@@ -205,14 +203,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The weighted values of one slot, this lane's value column, as three
   // planes in the slot's buffer.
   auto weigh = [&](int it, int slot) {
-    const int use = slot_use(slot, it), buf = slot_buffer(slot);
-    // A wait by parity has to come within one phase of its barrier. Where two
-    // slots take turns in a buffer, each warpgroup has waited for a later
-    // product of the chunk before; only the third one without outputs has
-    // not, and does it here.
-    if (STATE_ONLY && slot == 2 && it > 0 && !wait(kUpdate, it - 1))
-      return false;
-    if (use > 0 && !wait(kUsed + buf, use - 1)) return false;
+    // the buffer is free: slot 0 and 2 follow the whole last chunk (which the
+    // second warpgroup has waited for), 1 its last use, 3 and 4 the slots
+    // before them in their buffers
+    const int buf = slot_buffer(slot);
+    if (slot == 0 && it > 0 && !wait(kUpdate, it - 1)) return false;
+    if (slot == 1 && it > 0 && !wait(kUsed + 1, it - 1)) return false;
+    if (slot >= 3 && !wait(kUsed + buf, it)) return false;
     if (r / 32 * 32 < TV) {
       tc::after_sync();
       const int t0 = slot_step(slot), groups = slot_groups(slot);
@@ -357,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc::mma_ts(e, tmem + L_::U, w + 8 * n, k, kUpdateShape, true);
               tc::mma_ts(e, tmem + L_::U, w, k, kUpdateShape, true);
             }
-            tc::commit(e, bar(kUsed + buf));
+            if (slot < 3) tc::commit(e, bar(kUsed + slot));
             if constexpr (!STATE_ONLY) {
               if (slot == 1) {
                 if (it > 0) alive = wait(kOutRead, it - 1);
@@ -538,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int it = 0; it < n_live; ++it) {
       if (!chunk_in(it) || (it == ragged && !wait(kClean, 0)) ||
-          !weigh(it, 1))
+          !weigh(it, 0))
         break;
       tc::bar_arrive(bar(kWeightsFree0 + (it & 1)));
       if constexpr (STATE_ONLY) continue;
@@ -677,44 +674,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     float seg_keep = 1.0f;
     put_state();
-    // In turn: the first slot of chunk it, the update by chunk it - 1 (whose
-    // products are under way meanwhile), the last slot of chunk it.
     bool alive = fit;
 #pragma unroll 1
-    for (int i = 0; alive && i < 2 * n_live + 1; ++i) {
-      const int it = i / 2, st = it & 1;
-      if (it < n_live) {
-        if (i % 2 == 0) {
-          alive = chunk_in(it);
-          if (alive && it == ragged) {
-            // rows behind the sequence's end: zeros, whatever was loaded
-            unsigned char *Ks = smem + st * L_::STAGE, *Vs = Ks + L_::Q;
-            const int dead_from = int(len - low(it));
+    for (int it = 0; alive && it < n_live; ++it) {
+      const int st = it & 1;
+      alive = chunk_in(it);
+      if (alive && it == ragged) {
+        // rows behind the sequence's end: zeros, whatever was loaded
+        unsigned char *Ks = smem + st * L_::STAGE, *Vs = Ks + L_::Q;
+        const int dead_from = int(len - low(it));
 #pragma unroll 1
-            for (int z = r + dead_from * 8; z < kChunk * 8; z += 128) {
+        for (int z = r + dead_from * 8; z < kChunk * 8; z += 128) {
 #pragma unroll
-              for (int c = 0; c < QD / 64; ++c)
-                *reinterpret_cast<uint4 *>(Ks + c * 16384 + z * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
+          for (int c = 0; c < QD / 64; ++c)
+            *reinterpret_cast<uint4 *>(Ks + c * 16384 + z * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-              for (int c = 0; c < TV / 64; ++c)
-                *reinterpret_cast<uint4 *>(Vs + c * 16384 + z * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            }
-            tc::fence_async();
-            tc::bar_arrive(bar(kClean));
-            alive = wait(kClean, 0);
-          }
+          for (int c = 0; c < TV / 64; ++c)
+            *reinterpret_cast<uint4 *>(Vs + c * 16384 + z * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
         }
-        alive = alive && weigh(it, i % 2 == 0 ? 0 : 4);
-        if (!alive) break;
+        tc::fence_async();
+        tc::bar_arrive(bar(kClean));
+        alive = wait(kClean, 0);
       }
-      if (i % 2 == 1 || it == 0) continue;
-      const int done = it - 1;
-      const float keep = gt.keep[done & 1];
+#pragma unroll 1
+      for (int slot = 2; slot < 5 && alive; ++slot) alive = weigh(it, slot);
+      if (!alive) break;
+      const float keep = gt.keep[st];
       seg_keep *= keep;
-      tc::bar_arrive(bar(kWeightsFree0 + (done & 1)));
-      alive = wait(kUpdate, done);
+      tc::bar_arrive(bar(kWeightsFree0 + st));
+      alive = wait(kUpdate, it);
       if (!alive) break;
       tc::after_sync();
       if (keep == 0.0f) {  // a restart forgets the state whatever it held
@@ -784,10 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = 0; it < n_live; ++it) {
         const int st = it & 1;
         if (!chunk_in(it) || (it == ragged && !wait(kClean, 0))) break;
-        bool alive = true;
-#pragma unroll 1
-        for (int slot = 2; slot < 4 && alive; ++slot) alive = weigh(it, slot);
-        if (!alive) break;
+        if (!weigh(it, 1)) break;
         tc::bar_arrive(bar(kWeightsFree0 + st));
         if constexpr (STATE_ONLY) continue;
         // O1, scaled in its place: O2 is added to it there
