@@ -3,14 +3,15 @@ device, buffers allocated where the launch will use them."""
 from __future__ import annotations
 
 
-def dtype_code(t):
+def dtype_codes():
+    """The activation types by torch's name."""
     import torch
     from . import SSM_BF16, SSM_F32
-    if t.dtype == torch.bfloat16:
-        return SSM_BF16
-    if t.dtype == torch.float32:
-        return SSM_F32
-    raise TypeError("activations must be float32 or bfloat16")
+    return {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16}
+
+
+def dtype_error():
+    return TypeError("activations must be float32 or bfloat16")
 
 
 def dense(name, t, shape, dtype, device):
@@ -38,19 +39,17 @@ def apart(**tensors):
             raise ValueError("%s and %s must not overlap" % (a, b))
 
 
-def launch(device, stream, call, *args):
+def launch(torch, device, stream, call, *args):
     """call(raw stream, *args) with `device` current and torch's allocations
     made on that stream (so that a workspace or a result is never handed to,
     or taken from, work that another stream still has to do). stream: None
     for torch's current stream of the device, a torch stream or a raw one."""
-    import torch
+    index = device.index
     if stream is None:
-        if torch.cuda.current_device() == device.index:
-            return call(torch._C._cuda_getCurrentRawStream(device.index),
-                        *args)
+        if torch.cuda.current_device() == index:
+            return call(torch._C._cuda_getCurrentRawStream(index), *args)
         with torch.cuda.device(device):
-            return call(torch._C._cuda_getCurrentRawStream(device.index),
-                        *args)
+            return call(torch._C._cuda_getCurrentRawStream(index), *args)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
     if stream.device != device:

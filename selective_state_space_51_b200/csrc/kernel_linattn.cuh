@@ -348,14 +348,13 @@ __global__ void __launch_bounds__(kThreads, MINB)
 
   const LaJob &job = p.job[blockIdx.y];
   // tiles of one head, then heads, are neighbours: they read the same q and k
-  int64_t x = blockIdx.x;
-  const int tile = int(x % job.tiles);
-  x /= job.tiles;
-  const int h = int(x % p.heads);
-  x /= p.heads;
-  const int64_t b = x % p.batch;
-  const int seg = int(x / p.batch);
-  if (seg >= p.nseg) return;
+  unsigned x = blockIdx.x;
+  const int tile = int(x % unsigned(job.tiles));
+  x /= unsigned(job.tiles);
+  const unsigned local = x % unsigned(p.bhs);
+  const int seg = int(x / unsigned(p.bhs));
+  const int h = int((p.bh0 + local) % unsigned(p.heads));
+  const int64_t b = (p.bh0 + local) / unsigned(p.heads);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int wm = warp % 4, wn = warp / 4;
@@ -388,7 +387,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
   constexpr int64_t SF = int64_t(QD) * kLaTile;
   float *seg_state =
       p.nseg > 1
-          ? job.seg_state + ((bh * p.nseg + seg) * job.tiles + tile) * SF
+          ? job.seg_state +
+                ((int64_t(local) * p.nseg + seg) * job.tiles + tile) * SF
           : nullptr;
 
   float S[NT][4];
@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
           make_float2(S[n][2 * hr], S[n][2 * hr + 1]);
     });
     if (tile == 0 && threadIdx.x == 0)
-      job.seg_decay[bh * p.nseg + seg] = seg_keep;
+      job.seg_decay[int64_t(local) * p.nseg + seg] = seg_keep;
   } else if (job.last && seg == p.nseg - 1) {
     // running backwards, the first token's own decay is still to come
     float f = 1.0f;
@@ -811,16 +811,16 @@ __global__ void __launch_bounds__(256)
   constexpr int64_t SF = int64_t(QD) * kLaTile;
   const int64_t per = SF * job.tiles;
   const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (e >= per * p.batch * p.heads) return;
-  const int64_t bh = e / per, el = e % per;
+  if (e >= per * p.bhs) return;
+  const int64_t local = e / per, bh = p.bh0 + local, el = e % per;
   const int tile = int(el / SF), row = int(el % SF / kLaTile),
             col = int(el % kLaTile) + tile * kLaTile;
   float S = 0.0f;
   if (job.init && row < job.qd && col < job.vd)
     S = job.init[bh * job.qd * job.vd + int64_t(row) * job.state_rs +
                  int64_t(col) * job.state_cs];
-  float *u = job.seg_state + bh * p.nseg * per + el;
-  const float *d = job.seg_decay + bh * p.nseg;
+  float *u = job.seg_state + local * p.nseg * per + el;
+  const float *d = job.seg_decay + local * p.nseg;
   int m = 0;
   const int n = p.nseg - 1;
   for (; m + 4 <= n; m += 4) {

@@ -135,11 +135,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const LaJob &job = p.job[blockIdx.y];
   const CUtensorMap *maps = pp.map[blockIdx.y];
 
-  unsigned x = blockIdx.x;
-  const int h = int(x % unsigned(p.heads));
-  x /= unsigned(p.heads);
-  const int64_t b = x % unsigned(p.batch);
-  const int seg = int(x / unsigned(p.batch));
+  const unsigned local = blockIdx.x % unsigned(p.bhs);
+  const int seg = int(blockIdx.x / unsigned(p.bhs));
+  const int h = int((p.bh0 + local) % unsigned(p.heads));
+  const int64_t b = (p.bh0 + local) / unsigned(p.heads);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t L = p.seqlen;
   int64_t len = L;
@@ -626,7 +625,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     float *seg_state =
         p.nseg > 1 && r / kLaTile < tiles
             ? job.seg_state +
-                  ((bh * p.nseg + seg) * tiles + r / kLaTile) * SF +
+                  ((int64_t(local) * p.nseg + seg) * tiles + r / kLaTile) *
+                      SF +
                   r % kLaTile
             : nullptr;
     float S[QD];
@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (STATE_ONLY) {
       dst = seg_state;
       keys = QD;
-      if (r == 0) job.seg_decay[bh * p.nseg + seg] = seg_keep;
+      if (r == 0) job.seg_decay[int64_t(local) * p.nseg + seg] = seg_keep;
     } else if (job.last && seg == p.nseg - 1 && r < job.vd) {
       dst = job.last + bh * job.qd * job.vd + int64_t(r) * job.state_cs;
       keys = job.qd;

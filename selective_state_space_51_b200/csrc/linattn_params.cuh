@@ -33,8 +33,8 @@ struct LaJob {
   int dot_heads;
   float *rows;                           // [2 tiles, b, heads, L] row dots,
                                          // of 32 columns each
-  float *seg_state;                      // [b, heads, nseg, tiles, QD, 64]
-  float *seg_decay;                      // [b, heads, nseg]
+  float *seg_state;                      // [bhs, nseg, tiles, QD, 64]
+  float *seg_decay;                      // [bhs, nseg]
 };
 
 struct LaParams {
@@ -46,6 +46,8 @@ struct LaParams {
   int heads;
   int nseg;                     // segments per sequence
   int64_t seg_len;              // steps per segment, a multiple of the chunk
+  int bh0, bhs;                 // the sequences' heads of this launch, counted
+                                // through all: bhs of them from bh0 on
 };
 
 // The log decay's gradient from the row dots and the states at the segments'

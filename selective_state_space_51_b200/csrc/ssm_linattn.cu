@@ -57,6 +57,7 @@ int check_dims(ssm_linattn_dims *d, int dtype, int64_t max_value) {
   if (__builtin_mul_overflow(d->batch * d->heads, d->dk * d->dv, &st) ||
       st > kMaxElements)
     return SSM_ERR_INVALID;
+  if (d->batch * d->heads > 0x7fffffff) return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }
 
@@ -67,6 +68,9 @@ enum class Path { kAny, kTc };
 struct Plan {
   int nseg = 1;
   int64_t seg_len = 0;
+  // heads that run uncut before the others, which are cut (forward)
+  int64_t whole = 0;
+  int64_t whole_len = 0;
   // byte offsets into the workspace; jobs: y or dq, dk, dv
   size_t state[3] = {0, 0, 0}, decay[3] = {0, 0, 0};
   size_t part_dq = 0, part_dk = 0, rows_q = 0, rows_k = 0, part_head = 0,
@@ -101,10 +105,24 @@ void cut(Plan *pl, int64_t blocks, int64_t L, int sms, Path path,
 Plan plan_fwd(const ssm_linattn_dims &d, Path path, int sms) {
   Plan pl;
   const int64_t tiles = ceil_div(d.dv, ssm::kLaTile);
-  cut(&pl, d.batch * d.heads * (path == Path::kTc ? 1 : tiles), d.seqlen, sms,
-      path, int64_t(1) << 40);
+  const int64_t all = d.batch * d.heads;
+  // One block an SM: where the last round of blocks would leave over half of
+  // the SMs idle, its heads are cut (4 x 8192 x 40 heads of 128: 550 us with
+  // 12 heads in a round of their own, %TAIL% with these cut).
+  auto cut_for = [&](int64_t heads) {
+    cut(&pl, heads * (path == Path::kTc ? 1 : tiles), d.seqlen, sms, path,
+        int64_t(1) << 40);
+  };
+  cut_for(all);
+  if (path == Path::kTc && all > sms && all % sms != 0) {
+    cut_for(all % sms);
+    if (pl.nseg > 1) pl.whole = all / sms * sms;
+    else cut_for(all);
+  }
+  pl.whole_len =
+      ceil_div(d.seqlen, ssm::lat::kChunk) * ssm::lat::kChunk;
   if (pl.nseg > 1) {
-    const size_t bh = size_t(d.batch) * d.heads;
+    const size_t bh = size_t(all - pl.whole);
     pl.state[0] = take(&pl.bytes, bh * pl.nseg * tiles * key_pad(d.dk) *
                                       ssm::kLaTile);
     pl.decay[0] = take(&pl.bytes, bh * pl.nseg);
@@ -146,7 +164,7 @@ int launch_jobs(const LaParams &p, int n, cudaStream_t s) {
   int tiles = 0;
   for (int j = 0; j < n; ++j) tiles = std::max(tiles, p.job[j].tiles);
   // jobs of one launch have the same tile count (the caller groups them)
-  const int64_t one = int64_t(tiles) * p.heads * p.batch;
+  const int64_t one = int64_t(tiles) * p.bhs;
   if (one > 0x7fffffff / p.nseg) return SSM_ERR_UNSUPPORTED;
   if (p.nseg > 1) {
     auto kern = ssm::la::linattn_kernel<T, NP, PS, QD, true, MINB>;
@@ -232,7 +250,7 @@ bool tc_takes(const ssm_linattn_dims &d, int dtype, const void *q,
 template <int QD, int TV, int PS>
 int launch_tc(const ssm::lat::Params &pp, int n, cudaStream_t s) {
   const LaParams &p = pp.p;
-  const int64_t one = int64_t(p.heads) * p.batch;
+  const int64_t one = p.bhs;
   if (one > 0x7fffffff / p.nseg) return SSM_ERR_UNSUPPORTED;
   if (p.nseg > 1) {
     auto kern = ssm::lat::linattn_tc_kernel<QD, TV, 1, true>;
@@ -320,6 +338,7 @@ LaParams common(const ssm_linattn_dims &d, const Plan &pl,
   p.heads = int(d.heads);
   p.nseg = pl.nseg;
   p.seg_len = pl.seg_len;
+  p.bhs = int(d.batch * d.heads);
   return p;
 }
 
@@ -405,8 +424,18 @@ int ssm_linattn_fwd(int device, const void *q, const void *k, const void *v,
     j.seg_decay = reinterpret_cast<float *>(ws + pl.decay[0]);
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return path == Path::kTc ? run_tc(p, 1, false, device, s)
-                           : run_jobs(p, 1, dtype, false, s);
+  if (path == Path::kAny) return run_jobs(p, 1, dtype, false, s);
+  if (pl.whole > 0) {
+    LaParams first = p;
+    first.nseg = 1;
+    first.seg_len = pl.whole_len;
+    first.bhs = int(pl.whole);
+    rc = run_tc(first, 1, false, device, s);
+    if (rc != SSM_OK) return rc;
+    p.bh0 = int(pl.whole);
+    p.bhs -= int(pl.whole);
+  }
+  return run_tc(p, 1, false, device, s);
 }
 
 int ssm_linattn_step(int device, const void *q, const void *k, const void *v,

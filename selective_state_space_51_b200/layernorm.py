@@ -4,7 +4,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _check, _ptr, _stream, library
-from ._launch import dense, dtype_code, launch, ptr
+from ._launch import dense, dtype_codes, dtype_error, launch, ptr
 
 
 def ssm_layernorm_workspace(device, rows, dim, dtype) -> int:
@@ -49,33 +49,43 @@ class LayerNorm:
 
     def __init__(self, device: int = 0):
         import torch
+        self._torch = torch
         self._lib = library()
+        self._codes = dtype_codes()
         self.device = torch.device("cuda", int(device))
         self._bytes = {}
 
     def _rows(self, x):
-        if x.dim() < 1 or x.numel() == 0:
+        """x's type, rows and their width."""
+        code, n = self._codes.get(x.dtype), x.numel()
+        if code is None:
+            raise dtype_error()
+        if n == 0 or x.dim() < 1:
             raise ValueError("x must have at least one row")
-        return x.numel() // x.shape[-1], x.shape[-1]
+        dim = x.shape[-1]
+        return code, n // dim, dim
 
     def __call__(self, x, weight=None, bias=None, residual=None, eps=1e-5,
                  y=None, stream=None):
         """Norms s = x + residual (rounded to x's type). Returns a dict: y,
         sum (None without residual), mean and rstd [rows] float32, which the
         backward pass takes."""
-        import torch
-        code = dtype_code(x)
-        rows, dim = self._rows(x)
+        torch = self._torch
+        code, rows, dim = self._rows(x)
         dense("x", x, x.shape, x.dtype, self.device)
-        dense("residual", residual, x.shape, x.dtype, self.device)
-        dense("y", y, x.shape, x.dtype, self.device)
-        dense("weight", weight, (dim,), torch.float32, self.device)
-        dense("bias", bias, (dim,), torch.float32, self.device)
-        return launch(self.device, stream, self._forward, x, weight, bias,
+        if residual is not None:
+            dense("residual", residual, x.shape, x.dtype, self.device)
+        if y is not None:
+            dense("y", y, x.shape, x.dtype, self.device)
+        if weight is not None:
+            dense("weight", weight, (dim,), torch.float32, self.device)
+        if bias is not None:
+            dense("bias", bias, (dim,), torch.float32, self.device)
+        return launch(torch, self.device, stream, self._forward, x, weight, bias,
                       residual, eps, y, rows, dim, code)
 
     def _forward(self, s, x, weight, bias, residual, eps, y, rows, dim, code):
-        import torch
+        torch = self._torch
         if y is None:
             y = torch.empty_like(x)
         total = None if residual is None else torch.empty_like(x)
@@ -93,25 +103,27 @@ class LayerNorm:
         forward's sum where there was a residual); mean, rstd: the forward's.
         Returns a dict: dx (of x, and of the residual), dweight, dbias
         (float32; None without weight / bias)."""
-        import torch
-        code = dtype_code(x)
-        rows, dim = self._rows(x)
+        torch = self._torch
+        code, rows, dim = self._rows(x)
         if dy is None or mean is None or rstd is None:
             raise ValueError("dy, mean and rstd are required")
         f32 = torch.float32
         dense("x", x, x.shape, x.dtype, self.device)
         dense("dy", dy, x.shape, x.dtype, self.device)
-        dense("dsum", dsum, x.shape, x.dtype, self.device)
+        if dsum is not None:
+            dense("dsum", dsum, x.shape, x.dtype, self.device)
         dense("mean", mean, (rows,), f32, self.device)
         dense("rstd", rstd, (rows,), f32, self.device)
-        dense("weight", weight, (dim,), f32, self.device)
-        dense("bias", bias, (dim,), f32, self.device)
-        return launch(self.device, stream, self._backward, dy, x, mean, rstd,
+        if weight is not None:
+            dense("weight", weight, (dim,), f32, self.device)
+        if bias is not None:
+            dense("bias", bias, (dim,), f32, self.device)
+        return launch(torch, self.device, stream, self._backward, dy, x, mean, rstd,
                       weight, bias, dsum, rows, dim, code)
 
     def _backward(self, s, dy, x, mean, rstd, weight, bias, dsum, rows, dim,
                   code):
-        import torch
+        torch = self._torch
         f = dict(dtype=torch.float32, device=self.device)
         dx = torch.empty_like(x)
         dweight = None if weight is None else torch.empty(dim, **f)

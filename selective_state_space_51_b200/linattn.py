@@ -4,7 +4,7 @@ from __future__ import annotations
 import ctypes
 
 from . import (_check, _ptr, _stream, library, ssm_linattn_dims)
-from ._launch import apart, dense, dtype_code, launch, ptr
+from ._launch import apart, dense, dtype_codes, dtype_error, launch, ptr
 
 
 def _dims(dims):
@@ -82,24 +82,28 @@ class LinearAttention:
 
     def __init__(self, device: int = 0):
         import torch
+        self._torch = torch
         self._lib = library()
+        self._codes = dtype_codes()
         self.device = torch.device("cuda", int(device))
         self._bytes = {}
 
-    def _rows(self, name, t, shape, dtype):
+    def _rows(self, name, t, shape, heads, d, dtype):
         """Elements from one token of `t` to the next; shape: (b, L, heads,
         size), or (b, heads, size) for one token."""
-        if t.shape != shape or t.dtype != dtype or t.device != self.device:
+        if t.shape != shape or t.dtype is not dtype or t.device != self.device:
             raise ValueError("%s must be a %s tensor of shape %s on %s" % (
                 name, dtype, tuple(shape), self.device))
+        dense_step = heads * d
+        if t.is_contiguous():
+            return dense_step
         s = t.stride()
-        heads, d = shape[-2:]
         if len(shape) == 4 and shape[1] > 1:
             step = s[1]
             even = shape[0] == 1 or s[0] == shape[1] * step
         else:
-            step, even = (s[0] if shape[0] > 1 else heads * d), True
-        if not (even and step >= heads * d and (d == 1 or s[-1] == 1)
+            step, even = (s[0] if shape[0] > 1 else dense_step), True
+        if not (even and step >= dense_step and (d == 1 or s[-1] == 1)
                 and (heads == 1 or s[-2] == d)):
             raise ValueError(
                 "%s must hold each token's heads in one piece, with one "
@@ -108,33 +112,35 @@ class LinearAttention:
 
     def _inputs(self, q, k, v, log_decay, head_log_decay, lengths, scale,
                 rank=4):
-        import torch
-        if q.dim() != rank or v.dim() != rank:
+        sq, sv, ty = q.shape, v.shape, q.dtype
+        if len(sq) != rank or len(sv) != rank:
             raise ValueError("q, k and v must have the dimensions [batch, "
                              "%sheads, size]" % ("tokens, " if rank == 4
                                                  else ""))
-        code, ty = dtype_code(q), q.dtype
-        sq, sv = q.shape, v.shape
+        code = self._codes.get(ty)
+        if code is None:
+            raise dtype_error()
         G, dk = sq[-2:]
         H, dv = sv[-2:]
         if sv[:-2] != sq[:-2] or G == 0 or H % G:
             raise ValueError("v must have q's tokens, and a multiple of its "
                              "heads")
-        L = sq[1] if rank == 4 else 1
-        dims = (sq[0], L, H, G, dk, dv, self._rows("q", q, sq, ty),
-                self._rows("k", k, sq, ty), self._rows("v", v, sv, ty))
+        rows = self._rows
+        dims = (sq[0], sq[1] if rank == 4 else 1, H, G, dk, dv,
+                rows("q", q, sq, G, dk, ty), rows("k", k, sq, G, dk, ty),
+                rows("v", v, sv, H, dv, ty))
         if log_decay is not None:
             dense("log_decay", log_decay, sv[:-1], ty, self.device)
         if head_log_decay is not None:
-            dense("head_log_decay", head_log_decay, (H,), torch.float32,
+            dense("head_log_decay", head_log_decay, (H,), self._torch.float32,
                   self.device)
         if lengths is not None:
-            dense("lengths", lengths, (sq[0],), torch.int32, self.device)
+            dense("lengths", lengths, (sq[0],), self._torch.int32, self.device)
         return dims, code, dk ** -0.5 if scale is None else scale
 
     def _workspace(self, dims, code, backward):
         """Allocated anew for each call, on its stream: nothing is shared."""
-        import torch
+        torch = self._torch
         key = (dims[:6], code, backward)
         n = self._bytes.get(key)
         if n is None:
@@ -147,7 +153,7 @@ class LinearAttention:
     def sync_status(self, stream=None) -> int:
         """Waits for the stream; SSM_OK unless a kernel's bounded wait gave
         up or the device has an error."""
-        return launch(self.device, stream, lambda s: ssm_linattn_sync_status(
+        return launch(self._torch, self.device, stream, lambda s: ssm_linattn_sync_status(
             self.device.index, s))
 
     def __call__(self, q, k, v, log_decay=None, head_log_decay=None,
@@ -155,7 +161,7 @@ class LinearAttention:
                  return_last_state=True, stream=None):
         """A prompt: y [b, L, H, dv], and the last state with
         return_last_state. h_last may be h0 itself."""
-        import torch
+        torch = self._torch
         dims, code, scale = self._inputs(q, k, v, log_decay, head_log_decay,
                                          lengths, scale)
         state = (dims[0], dims[2], dims[4], dims[5])
@@ -165,14 +171,14 @@ class LinearAttention:
         if h_last is not None and h0 is not None and \
                 h_last.data_ptr() != h0.data_ptr():
             apart(h0=h0, h_last=h_last)
-        y, h_last = launch(self.device, stream, self._prompt, q, k, v,
+        y, h_last = launch(self._torch, self.device, stream, self._prompt, q, k, v,
                            log_decay, head_log_decay, scale, lengths, h0, y,
                            h_last, return_last_state, dims, code)
         return (y, h_last) if return_last_state else y
 
     def _prompt(self, s, q, k, v, log_decay, head_log_decay, scale, lengths,
                 h0, y, h_last, want_last, dims, code):
-        import torch
+        torch = self._torch
         if y is None:
             y = torch.empty(v.shape, dtype=q.dtype, device=self.device)
         if h_last is None and want_last:
@@ -190,7 +196,7 @@ class LinearAttention:
              scale=None, y=None, stream=None):
         """One token of every sequence: q, k [b, G, dk], v [b, H, dv],
         log_decay [b, H]. state is updated in place. Returns y [b, H, dv]."""
-        import torch
+        torch = self._torch
         dims, code, scale = self._inputs(q, k, v, log_decay, head_log_decay,
                                          None, scale, rank=3)
         if state is None:
@@ -198,12 +204,12 @@ class LinearAttention:
         dense("state", state, (dims[0], dims[2], dims[4], dims[5]),
               torch.float32, self.device)
         dense("y", y, v.shape, q.dtype, self.device)
-        return launch(self.device, stream, self._step, q, k, v, state,
+        return launch(self._torch, self.device, stream, self._step, q, k, v, state,
                       log_decay, head_log_decay, scale, y, dims, code)
 
     def _step(self, s, q, k, v, state, log_decay, head_log_decay, scale, y,
               dims, code):
-        import torch
+        torch = self._torch
         if y is None:
             y = torch.empty(v.shape, dtype=q.dtype, device=self.device)
         _check(self._lib.ssm_linattn_step(
@@ -221,7 +227,7 @@ class LinearAttention:
         (activation dtype), dhead_log_decay, dh0 (float32). The decays'
         gradients are None without their inputs, or with decay_gradient=False
         (a fixed decay: fewer products)."""
-        import torch
+        torch = self._torch
         dims, code, scale = self._inputs(q, k, v, log_decay, head_log_decay,
                                          lengths, scale)
         if dy is None:
@@ -230,13 +236,13 @@ class LinearAttention:
         dense("dy", dy, v.shape, q.dtype, self.device)
         dense("h0", h0, state, torch.float32, self.device)
         dense("dh_last", dh_last, state, torch.float32, self.device)
-        return launch(self.device, stream, self._backward, q, k, v, dy,
+        return launch(self._torch, self.device, stream, self._backward, q, k, v, dy,
                       log_decay, head_log_decay, scale, lengths, h0, dh_last,
                       decay_gradient, dims, code)
 
     def _backward(self, s, q, k, v, dy, log_decay, head_log_decay, scale,
                   lengths, h0, dh_last, decay_gradient, dims, code):
-        import torch
+        torch = self._torch
         b, L, H, G, dk, dv = dims[:6]
         act = dict(dtype=q.dtype, device=self.device)
         f = dict(dtype=torch.float32, device=self.device)
