@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(512)
 constexpr int kFold = 32;
 
 template <typename T, int V, int N, int G>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(512, V == 1 && N <= 4 ? 2 : 1)
     layernorm_bwd_kernel(const __grid_constant__ NormParams p) {
   constexpr bool FOLD = N * V <= 8;
   __shared__ float2 red[64];
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(512)
     for (int j = 0; j < V; ++j) w[i][j] = 1.0f;
     if (c < p.dim && p.weight) load_param<V>(p.weight + c, w[i]);
   }
-  Raw<T, V> nx[N], ng[N], nd[N];
+  Raw<T, V> nx[N], ng[N];
   float nmean = 0.0f, nrstd = 0.0f;
   auto fetch = [&](int64_t st) {
     const int64_t row = st * per + group;
@@ -273,12 +273,10 @@ __global__ void __launch_bounds__(512)
       const int c = (i * lanes + lane) * V;
       nx[i].zero();
       ng[i].zero();
-      nd[i].zero();
       if (in && c < p.dim) {
         const int64_t at = row * p.dim + c;
         nx[i].load(static_cast<const T *>(p.x) + at);
         ng[i].load(static_cast<const T *>(p.dy) + at);
-        if (p.dsum) nd[i].load(static_cast<const T *>(p.dsum) + at);
       }
     }
   };
@@ -289,7 +287,16 @@ __global__ void __launch_bounds__(512)
     const bool in = row < p.rows;
     const int64_t base = row * p.dim;
     const float mean = nmean, rstd = nrstd;
-    float x[N][V], g[N][V], ds[N][V];
+    float x[N][V], g[N][V];
+    // (needed last: on its way while the row is summed)
+    Raw<T, V> ds[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * lanes + lane) * V;
+      ds[i].zero();
+      if (in && c < p.dim && p.dsum)
+        ds[i].load(static_cast<const T *>(p.dsum) + base + c);
+    }
     float su = 0.0f, sux = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -299,7 +306,6 @@ __global__ void __launch_bounds__(512)
       for (int j = 0; j < V; ++j) {
         x[i][j] = live ? (nx[i].at(j) - mean) * rstd : 0.0f;
         g[i][j] = ng[i].at(j);
-        ds[i][j] = nd[i].at(j);
         dw[i][j] = fmaf(g[i][j], x[i][j], dw[i][j]);
         db[i][j] += g[i][j];
         g[i][j] *= w[i][j];
@@ -318,7 +324,7 @@ __global__ void __launch_bounds__(512)
         float o[V];
 #pragma unroll
         for (int j = 0; j < V; ++j)
-          o[j] = fmaf(g[i][j] - su - x[i][j] * sux, rstd, ds[i][j]);
+          o[j] = fmaf(g[i][j] - su - x[i][j] * sux, rstd, ds[i].at(j));
         store<T, V>(static_cast<T *>(p.dx) + base + c, o);
       }
     }

@@ -976,22 +976,43 @@ __global__ void __launch_bounds__(256)
 
 // ---- one token: S <- a S + k (x) v in place, y = scale q S.
 // Bound by the state's bytes (read and written once). A block of 8 warps owns
-// one head and 32 W value columns; each warp takes every eighth key row, a
-// lane W columns of it, and the rows' parts of y are added through shared
-// memory in a fixed order.
-template <typename T, int W>
+// one head and LPR W value columns: LPR lanes (16 where 64 columns are all
+// there are) share a key row, W columns each, so that a warp takes 32 / LPR
+// rows at a time and a block 256 / LPR; eight of them a thread are on their
+// way at once, the first before anything else is read. The rows' parts of y
+// are added through shared memory in a fixed order.
+// 256 x 40 heads of 128 x 128 float32: 201 us, 6.7 TB/s.
+template <typename T, int W, int LPR>
 __global__ void __launch_bounds__(256)
     linattn_step_kernel(const __grid_constant__ LaStepParams p) {
+  constexpr int COLS = LPR * W, STEP = 256 / LPR, ROWS = 8;
   __shared__ float ks[kLaMaxKey], qs[kLaMaxKey];
-  __shared__ float part[8][32 * W];
-  const int tiles = (p.dv + 32 * W - 1) / (32 * W);
-  const int tile = int(blockIdx.x % tiles);
-  const int64_t bh = blockIdx.x / tiles;
+  __shared__ float part[8][COLS];
+  const int tiles = (p.dv + COLS - 1) / COLS;
+  const int tile = int(blockIdx.x % unsigned(tiles));
+  const int64_t bh = blockIdx.x / unsigned(tiles);
   const int64_t b = bh / p.heads;
   const int h = int(bh % p.heads), g = h / (p.heads / p.groups);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int c0 = tile * 32 * W + lane * W;
+  const int first = threadIdx.x / LPR, at = lane % LPR * W;
+  const int c0 = tile * COLS + at;
   float *S = p.state + bh * p.dk * p.dv + c0;
+  float x[ROWS][W];
+  auto fetch = [&](int r0) {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const int r = r0 + STEP * i;
+      if (r >= p.dk || c0 >= p.dv) break;
+      const float *s = S + int64_t(r) * p.dv;
+      if constexpr (W == 4) {
+        const float4 u = __ldcs(reinterpret_cast<const float4 *>(s));
+        x[i][0] = u.x; x[i][1] = u.y; x[i][2] = u.z; x[i][3] = u.w;
+      } else {
+        x[i][0] = s[0];
+      }
+    }
+  };
+  fetch(first);
   const T *kp = static_cast<const T *>(p.k) + b * p.k_stride + g * p.dk;
   const T *qp = static_cast<const T *>(p.q) + b * p.q_stride + g * p.dk;
   const T *vp = static_cast<const T *>(p.v) + b * p.v_stride + h * p.dv + c0;
@@ -1011,34 +1032,35 @@ __global__ void __launch_bounds__(256)
     y[j] = 0.0f;
   }
   __syncthreads();
-  if (c0 < p.dv) {
-#pragma unroll 4
-    for (int r = warp; r < p.dk; r += 8) {
-      float *s = S + int64_t(r) * p.dv;
-      float x[W];
-      if constexpr (W == 4) {
-        const float4 u = *reinterpret_cast<const float4 *>(s);
-        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-      } else {
-        x[0] = s[0];
-      }
+#pragma unroll 1
+  for (int r0 = first; r0 < p.dk; r0 += STEP * ROWS) {
+    if (r0 != first) fetch(r0);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const int r = r0 + STEP * i;
+      if (r >= p.dk || c0 >= p.dv) break;
 #pragma unroll
       for (int j = 0; j < W; ++j) {
         // a = 0 starts anew, whatever the state held
-        x[j] = a == 0.0f ? ks[r] * v[j] : fmaf(a, x[j], ks[r] * v[j]);
-        y[j] = fmaf(qs[r], x[j], y[j]);
+        x[i][j] = a == 0.0f ? ks[r] * v[j] : fmaf(a, x[i][j], ks[r] * v[j]);
+        y[j] = fmaf(qs[r], x[i][j], y[j]);
       }
+      float *s = S + int64_t(r) * p.dv;
       if constexpr (W == 4)
-        *reinterpret_cast<float4 *>(s) = make_float4(x[0], x[1], x[2], x[3]);
+        __stcs(reinterpret_cast<float4 *>(s),
+               make_float4(x[i][0], x[i][1], x[i][2], x[i][3]));
       else
-        s[0] = x[0];
+        s[0] = x[i][0];
     }
   }
 #pragma unroll
-  for (int j = 0; j < W; ++j) part[warp][lane * W + j] = y[j];
+  for (int j = 0; j < W; ++j) {
+    if (LPR == 16) y[j] += __shfl_xor_sync(0xffffffffu, y[j], 16);
+    if (lane < LPR) part[warp][at + j] = y[j];
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < 32 * W; i += 256) {
-    const int c = tile * 32 * W + i;
+  for (int i = threadIdx.x; i < COLS; i += 256) {
+    const int c = tile * COLS + i;
     if (c < p.dv) {
       float s = 0.0f;
 #pragma unroll

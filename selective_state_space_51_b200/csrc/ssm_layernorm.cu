@@ -42,17 +42,17 @@ Shape shape_of(int dim, int v) {
   return s;
 }
 
-// Blocks the backward pass runs on (and partial rows it leaves): what is
-// resident at once, or one for each step of rows if there are fewer.
+// Most blocks the backward pass runs on (and partial rows it leaves): what
+// may be resident at once, or one for each step of rows if there are fewer.
 int parts_of(const Shape &s, int64_t rows, int sms) {
-  const int per_sm = std::max(1, 1024 / s.threads);
+  const int per_sm = std::max(1, 1536 / s.threads);
   return int(std::min<int64_t>(ceil_div(rows, s.per), int64_t(sms) * per_sm));
 }
 
 // Blocks of `threads` that an SM holds at once.
-int resident(const void *kern, int threads) {
+int resident(const void *kern, int threads, size_t smem = 0) {
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0) !=
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) !=
           cudaSuccess ||
       n < 1) {
     cudaGetLastError();
@@ -73,7 +73,7 @@ int launch_fwd(const NormParams &p, const Shape &s, int sms, cudaStream_t st) {
 }
 
 template <typename T, int V, int N, int G>
-int launch_bwd(const NormParams &p, const Shape &s, cudaStream_t st) {
+int launch_bwd(NormParams p, const Shape &s, int sms, cudaStream_t st) {
   auto kern = ssm::norm::layernorm_bwd_kernel<T, V, N, G>;
   const size_t smem =
       p.part ? size_t(s.per - 1) * 2 * p.dim * sizeof(float) : 0;
@@ -83,6 +83,9 @@ int launch_bwd(const NormParams &p, const Shape &s, cudaStream_t st) {
     cudaGetLastError();
     return SSM_ERR_CUDA;
   }
+  p.parts = std::min(p.parts,
+                     sms * resident(reinterpret_cast<const void *>(kern),
+                                    s.threads, smem));
   kern<<<unsigned(p.parts), s.threads, smem, st>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SSM_ERR_CUDA;
   if (!p.part) return SSM_OK;
@@ -93,7 +96,7 @@ int launch_bwd(const NormParams &p, const Shape &s, cudaStream_t st) {
 
 template <typename T, int V, bool BWD, int N, int G>
 int launch(const NormParams &p, const Shape &s, int sms, cudaStream_t st) {
-  if constexpr (BWD) return launch_bwd<T, V, N, G>(p, s, st);
+  if constexpr (BWD) return launch_bwd<T, V, N, G>(p, s, sms, st);
   else return launch_fwd<T, V, N, G>(p, s, sms, st);
 }
 

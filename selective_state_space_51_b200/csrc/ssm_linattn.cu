@@ -463,15 +463,18 @@ int ssm_linattn_step(int device, const void *q, const void *k, const void *v,
   p.groups = int(dims.groups); p.dk = int(dims.dk); p.dv = int(dims.dv);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool wide = p.dv % 4 == 0 && aligned(state, 16);
+  const bool half = wide ? p.dv <= 64 : p.dv <= 16;
   const int64_t grid =
-      p.batch * p.heads * ceil_div(p.dv, wide ? 128 : 32);
+      p.batch * p.heads * ceil_div(p.dv, (wide ? 4 : 1) * (half ? 16 : 32));
   if (grid > 0x7fffffff) return SSM_ERR_UNSUPPORTED;
-  auto kern =
-      dtype == SSM_F32
-          ? (wide ? ssm::la::linattn_step_kernel<float, 4>
-                  : ssm::la::linattn_step_kernel<float, 1>)
-          : (wide ? ssm::la::linattn_step_kernel<bf16, 4>
-                  : ssm::la::linattn_step_kernel<bf16, 1>);
+  auto pick = [&](auto type) {
+    using T = decltype(type);
+    return wide ? (half ? ssm::la::linattn_step_kernel<T, 4, 16>
+                        : ssm::la::linattn_step_kernel<T, 4, 32>)
+                : (half ? ssm::la::linattn_step_kernel<T, 1, 16>
+                        : ssm::la::linattn_step_kernel<T, 1, 32>);
+  };
+  auto kern = dtype == SSM_F32 ? pick(float()) : pick(bf16());
   kern<<<unsigned(grid), 256, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
