@@ -807,41 +807,43 @@ __global__ void __launch_bounds__(kThreads, MINB)
 template <int QD>
 __global__ void __launch_bounds__(256)
     linattn_join_kernel(const __grid_constant__ LaParams p) {
-  const LaJob &job = p.job[blockIdx.y];
-  constexpr int64_t SF = int64_t(QD) * kLaTile;
-  const int64_t per = SF * job.tiles;
-  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (e >= per * p.bhs) return;
-  const int64_t local = e / per, bh = p.bh0 + local, el = e % per;
-  const int tile = int(el / SF), row = int(el % SF / kLaTile),
-            col = int(el % kLaTile) + tile * kLaTile;
-  float S = 0.0f;
-  if (job.init && row < job.qd && col < job.vd)
-    S = job.init[bh * job.qd * job.vd + int64_t(row) * job.state_rs +
-                 int64_t(col) * job.state_cs];
-  float *u = job.seg_state + local * p.nseg * per + el;
-  const float *d = job.seg_decay + local * p.nseg;
-  int m = 0;
-  const int n = p.nseg - 1;
-  for (; m + 4 <= n; m += 4) {
-    float a[4], k[4];
+  const LaJob &job = p.job[blockIdx.z];
+  constexpr int SF = QD * kLaTile;
+  const int per = SF * job.tiles;
+  const int el = int(blockIdx.x) * 256 + int(threadIdx.x);
+  if (el >= per) return;
+  const int tile = el / SF, row = el % SF / kLaTile,
+            col = el % kLaTile + tile * kLaTile;
+  for (int64_t local = blockIdx.y; local < p.bhs; local += gridDim.y) {
+    const int64_t bh = p.bh0 + local;
+    float S = 0.0f;
+    if (job.init && row < job.qd && col < job.vd)
+      S = job.init[bh * job.qd * job.vd + int64_t(row) * job.state_rs +
+                   int64_t(col) * job.state_cs];
+    float *u = job.seg_state + local * p.nseg * per + el;  // (a segment: per)
+    const float *d = job.seg_decay + local * p.nseg;
+    int m = 0;
+    const int n = p.nseg - 1;
+    for (; m + 4 <= n; m += 4) {
+      float a[4], k[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      a[j] = u[(m + j) * per];
-      k[j] = d[m + j];
-    }
+      for (int j = 0; j < 4; ++j) {
+        a[j] = u[int64_t(m + j) * per];
+        k[j] = d[m + j];
+      }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      u[(m + j) * per] = S;
-      S = k[j] == 0.0f ? a[j] : fmaf(k[j], S, a[j]);
+      for (int j = 0; j < 4; ++j) {
+        u[int64_t(m + j) * per] = S;
+        S = k[j] == 0.0f ? a[j] : fmaf(k[j], S, a[j]);
+      }
     }
+    for (; m < n; ++m) {
+      const float a = u[int64_t(m) * per];
+      u[int64_t(m) * per] = S;
+      S = d[m] == 0.0f ? a : fmaf(d[m], S, a);
+    }
+    u[int64_t(n) * per] = S;
   }
-  for (; m < n; ++m) {
-    const float a = u[m * per];
-    u[m * per] = S;
-    S = d[m] == 0.0f ? a : fmaf(d[m], S, a);
-  }
-  u[n * per] = S;
 }
 
 __device__ __forceinline__ float block_sum(float v, float *red) {
