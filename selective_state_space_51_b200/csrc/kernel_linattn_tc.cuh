@@ -15,7 +15,7 @@
 // product that is added to it. They go through two buffers of 32 steps.
 //
 // Three warpgroups (a thread has one TMEM lane) share the chunk's 128 weighted
-// steps, which all need the same arithmetic, and have one task of their own
+// steps, which all need the same arithmetic, and have a task of their own
 // each: the first turns P into P', the second holds the state, the third
 // scales O1 in its place (O2 is added to it there) and hands y to a TMA store.
 // The weighted values pass through three buffers of 32, 32 and 16 steps: the
@@ -51,7 +51,8 @@ struct Params {
 };
 
 enum Bar {
-  kFull0, kFull1,      // q, k, v of a stage have arrived
+  kFull0, kFull1,      // k, v of a stage have arrived
+  kFullQ0, kFullQ1,    // its q
   kEmpty0, kEmpty1,    // the stage's products are done
   kScores,             // P
   kRead,               // O1
@@ -92,8 +93,8 @@ struct Gates {
 };
 
 // The slots a chunk's weighted values come in: the first step, 8-step groups,
-// the buffer. Slot 0 is the first warpgroup's, 1 the third's, the others the
-// second's.
+// the buffer. Slot 0 is the first warpgroup's, 1 the third's (which both fill
+// them ahead), the others the second's.
 __host__ __device__ constexpr int slot_step(int s) {
   return s < 3 ? s * 32 : s == 3 ? 80 : 112;
 }
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The weighted values of one slot, this lane's value column, as three
   // planes in the slot's buffer.
   auto weigh = [&](int it, int slot) {
-    // the buffer is free: slot 0 and 2 follow the whole last chunk (which the
+    // the buffer is free: slots 0 and 2 follow the whole last chunk (which the
     // second warpgroup has waited for), 1 its last use, 3 and 4 the slots
     // before them in their buffers
     const int buf = slot_buffer(slot);
@@ -264,54 +265,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int qh = h / (p.heads / job.q_heads);
       const int vh = h / (p.heads / job.v_heads);
       const bool staged = !STATE_ONLY && !job.y_f32;
+      // k and v come as soon as their stage's products are done; q, where y is
+      // staged in its place, once y has been read
       int it = 0;
 #pragma unroll 1
       for (; fit && it < n_live + 2; ++it) {
         const int st = it & 1;
         const uint32_t s = base + st * L_::STAGE, f = bar(kFull0 + st);
-        if (it >= 2) {
-          if (staged) {
-            if (!wait(kStaged, it - 2)) break;
-            if (lane == 0) {
-              const uint32_t y =
-                  L_::OVER_Q ? s + L_::Q + L_::V : base + L_::Y;
+        if (it < n_live) {
+          if (it >= 2 && !wait(kEmpty0 + st, it / 2 - 1)) break;
+          if (lane == 0) {
+            tc::bar_expect(f, L_::Q + L_::V);
 #pragma unroll 1
-              for (int c = 0; c * 64 < job.vd; ++c)
-                tc::store_box(&maps[3], y + c * 16384, c * 64, h, low(it - 2),
-                              int(b));
-              tc::store_read();
-              tc::bar_arrive(bar(kStored));
-            }
-            __syncwarp();
+            for (int c = 0; c < QD / 64; ++c)
+              tc::load_box(s + c * 16384, &maps[1], f, c * 64, kh, low(it),
+                           int(b));
+#pragma unroll 1
+            for (int c = 0; c < TV / 64; ++c)
+              tc::load_box(s + L_::Q + c * 16384, &maps[2], f, c * 64, vh,
+                           low(it), int(b));
           }
-          if (it < n_live && !wait(kEmpty0 + st, it / 2 - 1)) break;
+          __syncwarp();
+        }
+        if (STATE_ONLY) continue;
+        if (it >= 2 && staged) {
+          if (!wait(kStaged, it - 2)) break;
+          if (lane == 0) {
+            const uint32_t y = L_::OVER_Q ? s + L_::Q + L_::V : base + L_::Y;
+#pragma unroll 1
+            for (int c = 0; c * 64 < job.vd; ++c)
+              tc::store_box(&maps[3], y + c * 16384, c * 64, h, low(it - 2),
+                            int(b));
+            tc::store_read();
+            tc::bar_arrive(bar(kStored));
+          }
+          __syncwarp();
         }
         if (it < n_live && lane == 0) {
-          const int tok = low(it);
-          tc::bar_expect(f, L_::STAGE);
+          tc::bar_expect(bar(kFullQ0 + st), L_::Q);
 #pragma unroll 1
-          for (int c = 0; c < QD / 64; ++c) {
-            tc::load_box(s + c * 16384, &maps[1], f, c * 64, kh, tok, int(b));
-            if (!STATE_ONLY)
-              tc::load_box(s + L_::Q + L_::V + c * 16384, &maps[0], f, c * 64,
-                           qh, tok, int(b));
-          }
-#pragma unroll 1
-          for (int c = 0; c < TV / 64; ++c)
-            tc::load_box(s + L_::Q + c * 16384, &maps[2], f, c * 64, vh, tok,
-                         int(b));
+          for (int c = 0; c < QD / 64; ++c)
+            tc::load_box(s + L_::Q + L_::V + c * 16384, &maps[0],
+                         bar(kFullQ0 + st), c * 64, qh, low(it), int(b));
         }
         __syncwarp();
       }
       if (it < n_live + 2) {
         // given up: nothing may still be on its way into this block's memory
         gt.dead = 1;
-        const int loaded = it < n_live ? it : n_live;
+        const int loaded = it < n_live ? it + 1 : n_live;
 #pragma unroll 1
-        for (it = loaded > 2 ? loaded - 2 : 0; it < loaded; ++it)
+        for (it = loaded > 3 ? loaded - 3 : 0; it < loaded; ++it)
 #pragma unroll 1
-          for (int i = 0; i < 1 << 16; ++i)
-            if (tc::bar_try(bar(kFull0 + (it & 1)), uint32_t(it / 2) & 1u))
+          for (int i = 0; i < 1 << 12; ++i)
+            if (tc::bar_try(bar(kFull0 + (it & 1)), uint32_t(it / 2) & 1u) &&
+                (STATE_ONLY || tc::bar_try(bar(kFullQ0 + (it & 1)),
+                                           uint32_t(it / 2) & 1u)))
               break;
       }
     } else if (warp == 13) {
@@ -393,7 +402,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i < n_live) {
           const int st = i & 1;
           const uint64_t K = stage0 + st * kStage, Q = K + kQ;
-          alive = wait(kFull0 + st, i / 2) && (i != ragged || wait(kClean, 0));
+          alive = wait(kFull0 + st, i / 2) &&
+                  (STATE_ONLY || wait(kFullQ0 + st, i / 2)) &&
+                  (i != ragged || wait(kClean, 0));
           if (!alive) break;
           tc::after_sync();
           if constexpr (!STATE_ONLY) {
@@ -533,8 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tb = rev ? 3 - warp : warp;
 #pragma unroll 1
     for (int it = 0; it < n_live; ++it) {
-      if (!chunk_in(it) || (it == ragged && !wait(kClean, 0)) ||
-          !weigh(it, 0))
+      if (!chunk_in(it) || (it == ragged && !wait(kClean, 0)) || !weigh(it, 0))
         break;
       tc::bar_arrive(bar(kWeightsFree0 + (it & 1)));
       if constexpr (STATE_ONLY) continue;
@@ -543,61 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rs = gt.from[r], from = rs == kNoRestart ? 0 : rs;
       const float chi = gt.hi[r],
                   clo = __uint_as_float(uint32_t(gt.lo[r]) << 16);
-      float e = 0.0f;
-#pragma unroll 1
-      for (int sb = 0; sb < 8; ++sb) {     // 16 rows j
-        const int nb = sb / 2, jb = rev ? 3 - nb : nb;  // their 32; in time
-        uint32_t v[16];
-        if (jb <= tb) {
-          tc::tmem_ld16(mine + L_::P + sb * 16, v);
-          tc::tmem_wait_ld();
-        }
-        if (jb < tb) {
-          const int ref = rev ? nb * 32 : nb * 32 + 31;  // row of step r
-          e = from <= jb * 32 + 31
-                  ? ex2((chi - gt.hi[ref]) +
-                        (clo - __uint_as_float(uint32_t(gt.lo[ref]) << 16))) *
-                        job.sp
-                  : 0.0f;
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 f =
-                *reinterpret_cast<const float4 *>(gt.near + sb * 16 + i);
-            const float d[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              v[i + j] =
-                  __float_as_uint(__uint_as_float(v[i + j]) * (e * d[j]));
-          }
-        } else if (jb == tb) {
-          // rows of steps in [from, step] of this block of 32, as bits
-          const int lo_s = max(from - jb * 32, 0), hi_s = step - jb * 32;
-          uint32_t bits =
-              (0xffffffffu >> (31 - hi_s)) & (0xffffffffu << lo_s);
-          if (rev) bits = __brev(bits);
-          bits >>= (sb & 1) * 16;
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 fh =
-                *reinterpret_cast<const float4 *>(gt.hi + sb * 16 + i);
-            const uint2 fl =
-                *reinterpret_cast<const uint2 *>(gt.lo + sb * 16 + i);
-            const float dh[4] = {fh.x, fh.y, fh.z, fh.w};
-            const float dl[4] = {la::lo2(fl.x), la::hi2(fl.x), la::lo2(fl.y),
-                                 la::hi2(fl.y)};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float d = ex2((chi - dh[j]) + (clo - dl[j])) * job.sp;
-              v[i + j] = bits >> (i + j) & 1u
-                             ? __float_as_uint(__uint_as_float(v[i + j]) * d)
-                             : 0u;
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = 0u;
-        }
-        // P' takes the place of its 16 columns of P: 8 a plane
+      // P' takes the place of its 16 columns of P: 8 a plane
+      auto put = [&](int col, const uint32_t *v) {
         uint32_t w[PS][8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -609,7 +566,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int s = 0; s < PS; ++s)
-          tc::tmem_st8(mine + L_::P + sb * 16 + s * 8, w[s]);
+          tc::tmem_st8(mine + L_::P + col + s * 8, w[s]);
+      };
+#pragma unroll 1
+      for (int nb = 0; nb < 4; ++nb) {     // 32 rows j
+        const int jb = rev ? 3 - nb : nb;  // in time
+        uint32_t v[32];
+        if (jb < tb) {
+          tc::tmem_ld32(mine + L_::P + nb * 32, v);
+          const int ref = rev ? nb * 32 : nb * 32 + 31;  // row of step r
+          const float e =
+              from <= jb * 32 + 31
+                  ? ex2((chi - gt.hi[ref]) +
+                        (clo - __uint_as_float(uint32_t(gt.lo[ref]) << 16))) *
+                        job.sp
+                  : 0.0f;
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 f =
+                *reinterpret_cast<const float4 *>(gt.near + nb * 32 + i);
+            const float d[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              v[i + j] =
+                  __float_as_uint(__uint_as_float(v[i + j]) * (e * d[j]));
+          }
+          put(nb * 32, v);
+          put(nb * 32 + 16, v + 16);
+        } else if (jb == tb) {
+          // rows of steps in [from, step] of this block of 32, as bits
+          const int lo_s = max(from - jb * 32, 0), hi_s = step - jb * 32;
+          uint32_t bits =
+              (0xffffffffu >> (31 - hi_s)) & (0xffffffffu << lo_s);
+          if (rev) bits = __brev(bits);
+#pragma unroll 1
+          for (int c = nb * 32; c < nb * 32 + 32; c += 16, bits >>= 16) {
+            tc::tmem_ld16(mine + L_::P + c, v);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              const float4 fh =
+                  *reinterpret_cast<const float4 *>(gt.hi + c + i);
+              const uint2 fl = *reinterpret_cast<const uint2 *>(gt.lo + c + i);
+              const float dh[4] = {fh.x, fh.y, fh.z, fh.w};
+              const float dl[4] = {la::lo2(fl.x), la::hi2(fl.x),
+                                   la::lo2(fl.y), la::hi2(fl.y)};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float d = ex2((chi - dh[j]) + (clo - dl[j])) * job.sp;
+                v[i + j] = bits >> (i + j) & 1u
+                               ? __float_as_uint(__uint_as_float(v[i + j]) * d)
+                               : 0u;
+              }
+            }
+            put(c, v);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = 0u;
+#pragma unroll
+          for (int c = 0; c < 32; c += 8)
+            if (PS == 2 || c % 16 == 0)
+              tc::tmem_st8(mine + L_::P + nb * 32 + c, v);
+        }
       }
       tc::tmem_wait_st();
       tc::bar_arrive(bar(kGatesFree));
@@ -675,35 +695,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     float seg_keep = 1.0f;
     put_state();
     bool alive = fit;
+    // In turn: the slots of chunk it, the arrival of chunk it + 1, the update.
 #pragma unroll 1
-    for (int it = 0; alive && it < n_live; ++it) {
-      const int st = it & 1;
-      alive = chunk_in(it);
-      if (alive && it == ragged) {
-        // rows behind the sequence's end: zeros, whatever was loaded
-        unsigned char *Ks = smem + st * L_::STAGE, *Vs = Ks + L_::Q;
-        const int dead_from = int(len - low(it));
+    for (int it = -1; alive && it < n_live; ++it) {
 #pragma unroll 1
-        for (int z = r + dead_from * 8; z < kChunk * 8; z += 128) {
+      for (int slot = 2; slot < 5 && alive && it >= 0; ++slot)
+        alive = weigh(it, slot);
+      if (alive && it + 1 < n_live) {
+        alive = chunk_in(it + 1);
+        if (alive && it + 1 == ragged) {
+          // rows behind the sequence's end: zeros, whatever was loaded
+          unsigned char *Ks = smem + ((it + 1) & 1) * L_::STAGE,
+                        *Vs = Ks + L_::Q;
+          const int dead_from = int(len - low(it + 1));
+#pragma unroll 1
+          for (int z = r + dead_from * 8; z < kChunk * 8; z += 128) {
 #pragma unroll
-          for (int c = 0; c < QD / 64; ++c)
-            *reinterpret_cast<uint4 *>(Ks + c * 16384 + z * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < QD / 64; ++c)
+              *reinterpret_cast<uint4 *>(Ks + c * 16384 + z * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-          for (int c = 0; c < TV / 64; ++c)
-            *reinterpret_cast<uint4 *>(Vs + c * 16384 + z * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < TV / 64; ++c)
+              *reinterpret_cast<uint4 *>(Vs + c * 16384 + z * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          }
+          tc::fence_async();
+          tc::bar_arrive(bar(kClean));
+          alive = wait(kClean, 0);
         }
-        tc::fence_async();
-        tc::bar_arrive(bar(kClean));
-        alive = wait(kClean, 0);
       }
-#pragma unroll 1
-      for (int slot = 2; slot < 5 && alive; ++slot) alive = weigh(it, slot);
       if (!alive) break;
-      const float keep = gt.keep[st];
+      if (it < 0) continue;
+      const float keep = gt.keep[it & 1];
       seg_keep *= keep;
-      tc::bar_arrive(bar(kWeightsFree0 + st));
+      tc::bar_arrive(bar(kWeightsFree0 + (it & 1)));
       alive = wait(kUpdate, it);
       if (!alive) break;
       tc::after_sync();
@@ -770,13 +795,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      // In turn: O1 of chunk it is scaled, slot 1 of chunk it + 1 weighed
+      // (while the output's products run), chunk it put out.
 #pragma unroll 1
-      for (int it = 0; it < n_live; ++it) {
+      for (int it = -1; it < n_live; ++it) {
         const int st = it & 1;
-        if (!chunk_in(it) || (it == ragged && !wait(kClean, 0))) break;
-        if (!weigh(it, 1)) break;
-        tc::bar_arrive(bar(kWeightsFree0 + st));
-        if constexpr (STATE_ONLY) continue;
+        if (!STATE_ONLY && it >= 0) {
         // O1, scaled in its place: O2 is added to it there
         if (!wait(kGates, it) || !wait(kRead, it)) break;
         tc::after_sync();
@@ -799,6 +823,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::bar_arrive(bar(kGatesFree));
         tc::before_sync();
         tc::bar_arrive(bar(kReadDone));
+        }
+        if (it + 1 < n_live) {
+          if (!chunk_in(it + 1) || (it + 1 == ragged && !wait(kClean, 0)) ||
+              !weigh(it + 1, 1))
+            break;
+          tc::bar_arrive(bar(kWeightsFree0 + ((it + 1) & 1)));
+        }
+        if (STATE_ONLY || it < 0) continue;
         const int64_t t = low(it) + r;
         const bool live = t < len;
         const bool staged = !job.y_f32;
