@@ -822,25 +822,22 @@ __global__ void __launch_bounds__(256)
                    int64_t(col) * job.state_cs];
     float *u = job.seg_state + local * p.nseg * per + el;  // (a segment: per)
     const float *d = job.seg_decay + local * p.nseg;
-    int m = 0;
+    // sixteen segments' parts are on their way at a time
     const int n = p.nseg - 1;
-    for (; m + 4 <= n; m += 4) {
-      float a[4], k[4];
+    for (int m = 0; m < n; m += 16) {
+      float a[16], k[16];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        a[j] = u[int64_t(m + j) * per];
-        k[j] = d[m + j];
-      }
+      for (int j = 0; j < 16; ++j)
+        if (m + j < n) {
+          a[j] = u[int64_t(m + j) * per];
+          k[j] = d[m + j];
+        }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        u[int64_t(m + j) * per] = S;
-        S = k[j] == 0.0f ? a[j] : fmaf(k[j], S, a[j]);
-      }
-    }
-    for (; m < n; ++m) {
-      const float a = u[int64_t(m) * per];
-      u[int64_t(m) * per] = S;
-      S = d[m] == 0.0f ? a : fmaf(d[m], S, a);
+      for (int j = 0; j < 16; ++j)
+        if (m + j < n) {
+          u[int64_t(m + j) * per] = S;
+          S = k[j] == 0.0f ? a[j] : fmaf(k[j], S, a[j]);
+        }
     }
     u[int64_t(n) * per] = S;
   }

@@ -94,7 +94,8 @@ void cut(Plan *pl, int64_t blocks, int64_t L, int sms, Path path,
   const int64_t slots = int64_t(sms) * (path == Path::kTc ? 1 : 2);
   int64_t n = 1;
   if (blocks * 2 <= slots)
-    n = std::min(slots / blocks, std::max<int64_t>(1, L / (4 * chunk)));
+    n = std::min(slots / blocks,
+                 std::max<int64_t>(1, L / (path == Path::kTc ? 512 : 128)));
   n = std::max(n, ceil_div(L, most));
   const int64_t chunks = ceil_div(L, chunk);
   const int64_t per = ceil_div(chunks, n);
