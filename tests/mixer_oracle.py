@@ -12,7 +12,10 @@ absolute values add up to m (the same recurrence on |q|, |k|, |v|):
     and may truncate, 2^-23 of the running sum; an output of one chunk goes
     through at most 6 (128 + 64 + 64) / 16 = 96 of them, and the state in front
     through 6 * 64 / 16 = 24 and one product more for each chunk: (100 + 25
-    chunks) 2^-23 m. The exponentials add 2^-22 m for each chunk: 4 more.
+    chunks) 2^-23 m. The exponentials add 2^-22 m for each chunk: 4 more. (A
+    chunk here is 64 steps; one of 128 has 3 * 128 / 16 = 24 in its place.)
+  - the decay's gradient beside bfloat16 may come of two planes: a scored or
+    read term is then off by 2^-17 more, and its result is bfloat16.
 """
 import numpy as np
 
