@@ -209,7 +209,7 @@ __device__ __forceinline__ void prefetch_tile(const T *src, int64_t stride,
 // there (so that they stay finite and small) and nothing before it is read.
 // The sums are formed in 64 bits and kept as a pair of floats: a difference of
 // two of them is then exact to float32 however much the chunk decays.
-struct Gates {
+struct alignas(16) Gates {
   float hi[kLaChunk], lo[kLaChunk];  // c_i since the last restart
   int from[kLaChunk];                // the last restart at or before step i
   float read[kLaChunk];              // e^{c_i}, 0 behind a restart
@@ -300,7 +300,7 @@ struct Layout {
   static constexpr int Q = V + NP * TV;
   static constexpr int S = Q + (STATE_ONLY ? 0 : NP * TQ);
   static constexpr int END = S + (STATE_ONLY ? 0 : PS * TS);
-  static constexpr int BYTES = END * 2 + int(sizeof(Gates));
+  static constexpr int BYTES = END * 2 + 2 * int(sizeof(Gates));
 };
 
 // The state in the warps' accumulators, in the usual m16n8 layout. With 128
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
   bf16 *sm = reinterpret_cast<bf16 *>(smem_raw);
   bf16 *Ks = sm + Lay::K, *Vs = sm + Lay::V;
   bf16 *Qs = sm + Lay::Q, *Ss = sm + Lay::S;
-  Gates &gt = *reinterpret_cast<Gates *>(sm + Lay::END);
+  Gates *gates = reinterpret_cast<Gates *>(sm + Lay::END);
 
   const LaJob &job = p.job[blockIdx.y];
   // tiles of one head, then heads, are neighbours: they read the same q and k
@@ -426,7 +426,9 @@ __global__ void __launch_bounds__(kThreads, MINB)
     rows.len = len;
     return rows;
   };
+  bool ready = false;  // this chunk's decays are summed
   for (int ch = 0; ch < chunks; ++ch) {
+    Gates &gt = gates[ch & 1];
     const Rows rows = rows_of(ch);
     const int64_t lowest =
         job.reverse ? rows.first - (kLaChunk - 1) : rows.first;
@@ -463,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
           prefetch_tile(qb, job.q_stride, job.qd, next);
       }
       __syncthreads();  // the last chunk's reads are done
-      if (warp == 0) load_gates<T>(gt, p, rows, b, h, job.reverse);
+      if (warp == 0 && !ready) load_gates<T>(gt, p, rows, b, h, job.reverse);
       rk.template store<NP>(Ks);
       rv.template store<NP>(Vs);
       if constexpr (!STATE_ONLY) {
@@ -713,6 +715,12 @@ __global__ void __launch_bounds__(kThreads, MINB)
         }
       }
     }
+
+    // the next chunk's decays, by a warp whose rows have the fewest scores
+    ready = ch + 1 < chunks;
+    if (warp == 0 && ready)
+      load_gates<T>(gates[(ch + 1) & 1], p, rows_of(ch + 1), b, h,
+                    job.reverse);
 
     // ---- the state: S <- keep S + (weighted k)^T v
     const float keep = gt.keep;

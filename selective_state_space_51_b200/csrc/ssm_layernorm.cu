@@ -23,16 +23,19 @@ struct Shape {
   int threads = 256, per = 1;  // of a block; rows of a block
 };
 
-// A thread holds at most 2 groups of 16 bytes, or 4 single elements: more of
-// them cost residency (registers) than they save barriers. Rows wider than 16
-// warps' worth of that (the launch bound) take more.
-Shape shape_of(int dim, int v) {
+// A thread holds at most 2 groups of 16 bytes, or 8 single elements (4 where
+// bfloat16 ones are normed): more of them cost residency (registers) than they
+// save barriers, fewer the reverse (32768 x 511 float32, backward: 158 us for
+// twice the bytes with 8, 182 with 4, 236 with 2; 511 bfloat16, forward: 532
+// us with 4, 828 with 8). Rows wider than 16 warps' worth of that (the launch
+// bound) take more.
+Shape shape_of(int dim, int v, int singles) {
   Shape s;
   const int nv = int(ceil_div(dim, v));
   if (nv <= 16) {
     s.g = nv <= 4 ? 4 : nv <= 8 ? 8 : 16;
   } else {
-    const int most = std::max<int>(v == 1 ? 4 : 2, int(ceil_div(nv, 512)));
+    const int most = std::max<int>(v == 1 ? singles : 2, int(ceil_div(nv, 512)));
     s.wpr = int(ceil_div(nv, 32 * most));
     s.n = int(ceil_div(nv, 32 * s.wpr));
   }
@@ -154,8 +157,8 @@ bool wide_rows(int64_t dim, size_t esz,
 
 int width(bool wide, size_t esz) { return wide ? int(16 / esz) : 1; }
 
-Shape row_shape(int64_t dim, bool wide, size_t esz) {
-  return shape_of(int(dim), width(wide, esz));
+Shape row_shape(int64_t dim, bool wide, size_t esz, bool bwd) {
+  return shape_of(int(dim), width(wide, esz), bwd || esz == 4 ? 8 : 4);
 }
 
 }  // namespace
@@ -172,9 +175,9 @@ int ssm_layernorm_workspace(int device, int64_t rows, int64_t dim, int dtype,
   rc = ssm::device_sms(device, &sms);
   if (rc != SSM_OK) return rc;
   const size_t esz = dtype == SSM_F32 ? 4 : 2;
-  int parts = parts_of(row_shape(dim, false, esz), rows, sms);
+  int parts = parts_of(row_shape(dim, false, esz, true), rows, sms);
   if (dim * esz % 16 == 0)
-    parts = std::max(parts, parts_of(row_shape(dim, true, esz), rows, sms));
+    parts = std::max(parts, parts_of(row_shape(dim, true, esz, true), rows, sms));
   *bytes = size_t(parts) * 2 * dim * sizeof(float);
   return SSM_OK;
 }
@@ -202,7 +205,7 @@ int ssm_layernorm_fwd(int device, const void *x, const void *residual,
   p.y = y; p.sum = sum; p.mean = mean; p.rstd = rstd; p.eps = eps;
   p.rows = rows; p.dim = int(dim);
   const bool wide = wide_rows(dim, esz, {x, residual, y, sum, weight, bias});
-  const Shape s = row_shape(dim, wide, esz);
+  const Shape s = row_shape(dim, wide, esz, false);
   p.wpr = s.wpr;
   return run(p, wide, false, dtype, s, sms,
              reinterpret_cast<cudaStream_t>(stream));
@@ -233,7 +236,7 @@ int ssm_layernorm_bwd(int device, const void *dy, const void *x,
   p.dweight = dweight; p.dbias = dbias;
   p.rows = rows; p.dim = int(dim);
   const bool wide = wide_rows(dim, esz, {dy, x, dsum, dx, weight});
-  const Shape s = row_shape(dim, wide, esz);
+  const Shape s = row_shape(dim, wide, esz, true);
   p.wpr = s.wpr;
   p.parts = parts_of(s, rows, sms);
   if (dweight || dbias) {
