@@ -41,7 +41,8 @@ extern "C" {
  *   residual     : NULL means s = x (and sum must be NULL).
  *   weight, bias : NULL means 1 and 0.
  * y may be x or residual itself, and sum may too (each element is read before
- * it is written); y and sum must not overlap each other.
+ * it is written). Nothing else that is written may overlap anything
+ * (SSM_ERR_INVALID), y and sum each other included.
  */
 SSM_API int ssm_layernorm_fwd(int device, const void *x, const void *residual,
                               const float *weight, const float *bias,
@@ -65,7 +66,8 @@ SSM_API int ssm_layernorm_workspace(int device, int64_t rows, int64_t dim,
  *   dweight, dbias : NULL means not wanted.
  *   workspace  : at least ssm_layernorm_workspace bytes, used until the call
  *                is done on `stream`; NULL when neither sum is wanted.
- * dx may be dy or dsum itself.
+ * dx may be dy, x or dsum itself. Nothing else that is written may overlap
+ * anything (SSM_ERR_INVALID).
  */
 SSM_API int ssm_layernorm_bwd(int device, const void *dy, const void *x,
                               const float *mean, const float *rstd,

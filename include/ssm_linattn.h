@@ -29,6 +29,12 @@
  *     what stands behind is not read into any result, whatever it holds; the
  *     rows of y and of the gradients there are written as zeros, and h_last is
  *     the state behind the last token (h0 for an empty sequence).
+ *   - q, k and v are finite within the lengths. An infinity or NaN there
+ *     reaches all that depends on it, and may reach any row of its sequence
+ *     and head: the products of a chunk of 64 or 128 steps multiply what is
+ *     masked by 0.
+ *   - Buffers that must not overlap are taken from their first element to
+ *     their last; SSM_ERR_INVALID where two do.
  *   - `device` is the CUDA device of every pointer and must be current.
  *   - The calls keep nothing and allocate nothing: they may run at once on
  *     several streams and threads, each with its own workspace, and be captured
@@ -82,7 +88,7 @@ SSM_API int ssm_linattn_workspace(int device, ssm_linattn_dims dims, int dtype,
  *   h_last : NULL means the last state is not written. It may be h0.
  *   workspace : at least ssm_linattn_workspace bytes, 16-byte aligned, used
  *            until the call is done on `stream`; NULL where that is 0.
- * y must not overlap an input.
+ * y and h_last must not overlap each other or (else) an input.
  */
 SSM_API int ssm_linattn_fwd(int device, const void *q, const void *k,
                             const void *v, const void *log_decay,
@@ -112,10 +118,10 @@ SSM_API int ssm_linattn_step(int device, const void *q, const void *k,
  *   dlog_decay      : [batch, seqlen, heads] activation dtype, or NULL;
  *   dhead_log_decay : [heads] float32, or NULL; each only with its input.
  *            Without either, dq and dk take fewer products.
- *   dh0    : [batch, heads, dk, dv] float32, or NULL. It may be dh_last.
+ *   dh0    : [batch, heads, dk, dv] float32, or NULL.
  *   workspace : as above, for backward != 0.
  * The log decays' gradients at a token that starts the state anew are 0.
- * Other outputs must not overlap an input.
+ * No output may overlap another or an input.
  */
 SSM_API int ssm_linattn_bwd(int device, const void *q, const void *k,
                             const void *v, const void *log_decay,

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <initializer_list>
 
 #include "../../include/ssm_scan.h"
 
@@ -12,6 +13,31 @@ namespace ssm {
 
 inline bool aligned(const void *p, size_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) == 0;
+}
+
+// Device memory from `at` on (nullptr: none).
+struct Span {
+  const void *at;
+  size_t bytes;
+};
+
+// Whether something of `writes` shares memory with another entry of it or with
+// one of `reads` (`same`: but for reads that start where the write does, for
+// calls that read each element before they write it).
+inline bool clash(std::initializer_list<Span> writes,
+                  std::initializer_list<Span> reads, bool same = false) {
+  auto meet = [](const Span &a, const Span &b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at),
+                    y = reinterpret_cast<uintptr_t>(b.at);
+    return x && y && x < y + b.bytes && y < x + a.bytes;
+  };
+  for (const Span *w = writes.begin(); w != writes.end(); ++w) {
+    for (const Span *o = w + 1; o != writes.end(); ++o)
+      if (meet(*w, *o)) return true;
+    for (const Span &r : reads)
+      if (meet(*w, r) && !(same && w->at == r.at)) return true;
+  }
+  return false;
 }
 
 // The multiprocessor count of a B200; SSM_ERR_ARCH on another architecture.

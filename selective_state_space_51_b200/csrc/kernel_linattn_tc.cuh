@@ -101,7 +101,9 @@ __host__ __device__ constexpr int slot_step(int s) {
 __host__ __device__ constexpr int slot_groups(int s) {
   return s == 2 || s == 4 ? 2 : 4;
 }
-__host__ __device__ constexpr int slot_buffer(int s) { return s < 3 ? s : s == 3 ? 0 : 2; }
+__host__ __device__ constexpr int slot_buffer(int s) {
+  return s < 3 ? s : s == 3 ? 0 : 2;
+}
 
 template <int QD, int TV, int PS, bool STATE_ONLY>
 struct Lay {
@@ -779,8 +781,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     {
       // rows of y behind the sequence's last live chunk
 #pragma unroll 1
-      for (int64_t t = STATE_ONLY ? L : idle_low + r; t < seg_low + p.seg_len && t < L;
-           t += 128) {
+      for (int64_t t = STATE_ONLY ? L : idle_low + r;
+           t < seg_low + p.seg_len && t < L; t += 128) {
         const int64_t at = ((b * L + t) * p.heads + h) * job.vd;
         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
@@ -801,28 +803,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = -1; it < n_live; ++it) {
         const int st = it & 1;
         if (!STATE_ONLY && it >= 0) {
-        // O1, scaled in its place: O2 is added to it there
-        if (!wait(kGates, it) || !wait(kRead, it)) break;
-        tc::after_sync();
-        const float rd =
-            gt.from[r] == kNoRestart ? ex2(gt.hi[r]) * job.si : 0.0f;
+          // O1, scaled in its place: O2 is added to it there
+          if (!wait(kGates, it) || !wait(kRead, it)) break;
+          tc::after_sync();
+          const float rd =
+              gt.from[r] == kNoRestart ? ex2(gt.hi[r]) * job.si : 0.0f;
 #pragma unroll 1
-        for (int u = 0; u < TV; u += 32) {
-          uint32_t v[32];
-          tc::tmem_ld32(mine + L_::O + u, v);
-          tc::tmem_wait_ld();
-          // a restart forgets the state whatever it held
+          for (int u = 0; u < TV; u += 32) {
+            uint32_t v[32];
+            tc::tmem_ld32(mine + L_::O + u, v);
+            tc::tmem_wait_ld();
+            // a restart forgets the state whatever it held
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            v[i] = rd == 0.0f ? 0u
-                              : __float_as_uint(__uint_as_float(v[i]) * rd);
-          tc::tmem_st16(mine + L_::O + u, v);
-          tc::tmem_st16(mine + L_::O + u + 16, v + 16);
-        }
-        tc::tmem_wait_st();
-        tc::bar_arrive(bar(kGatesFree));
-        tc::before_sync();
-        tc::bar_arrive(bar(kReadDone));
+            for (int i = 0; i < 32; ++i)
+              v[i] = rd == 0.0f ? 0u
+                                : __float_as_uint(__uint_as_float(v[i]) * rd);
+            tc::tmem_st16(mine + L_::O + u, v);
+            tc::tmem_st16(mine + L_::O + u + 16, v + 16);
+          }
+          tc::tmem_wait_st();
+          tc::bar_arrive(bar(kGatesFree));
+          tc::before_sync();
+          tc::bar_arrive(bar(kReadDone));
         }
         if (it + 1 < n_live) {
           if (!chunk_in(it + 1) || (it + 1 == ragged && !wait(kClean, 0)) ||

@@ -197,6 +197,13 @@ int ssm_layernorm_fwd(int device, const void *x, const void *residual,
   for (const float *q : {weight, bias, static_cast<const float *>(mean),
                          static_cast<const float *>(rstd)})
     if (q && !aligned(q, 4)) return SSM_ERR_ALIGN;
+  const size_t all = size_t(rows) * dim * esz, row = dim * sizeof(float),
+               stats = size_t(rows) * sizeof(float);
+  if (ssm::clash({{y, all}, {sum, all}, {mean, stats}, {rstd, stats}},
+                 {{weight, row}, {bias, row}}) ||
+      ssm::clash({{mean, stats}, {rstd, stats}}, {{x, all}, {residual, all}}) ||
+      ssm::clash({{y, all}, {sum, all}}, {{x, all}, {residual, all}}, true))
+    return SSM_ERR_INVALID;
   int sms = 0;
   rc = ssm::device_ready(device, &sms);
   if (rc != SSM_OK) return rc;
@@ -227,6 +234,14 @@ int ssm_layernorm_bwd(int device, const void *dy, const void *x,
        {mean, rstd, weight, static_cast<const float *>(dweight),
         static_cast<const float *>(dbias)})
     if (q && !aligned(q, 4)) return SSM_ERR_ALIGN;
+  const size_t all = size_t(rows) * dim * esz, row = dim * sizeof(float),
+               stats = size_t(rows) * sizeof(float);
+  if (ssm::clash({{dx, all}, {dweight, row}, {dbias, row}},
+                 {{mean, stats}, {rstd, stats}, {weight, row}}) ||
+      ssm::clash({{dweight, row}, {dbias, row}},
+                 {{dy, all}, {x, all}, {dsum, all}}) ||
+      ssm::clash({{dx, all}}, {{dy, all}, {x, all}, {dsum, all}}, true))
+    return SSM_ERR_INVALID;
   int sms = 0;
   rc = ssm::device_ready(device, &sms);
   if (rc != SSM_OK) return rc;

@@ -21,7 +21,12 @@ using ssm::LaParams;
 using ssm::LaStepParams;
 using bf16 = __nv_bfloat16;
 
-constexpr int64_t kMaxElements = int64_t(1) << 56;
+// Beyond what a device holds: sizes up to these overflow no index.
+constexpr int64_t kMaxElements = int64_t(1) << 42;
+constexpr int64_t kMaxSteps = int64_t(1) << 36;
+// The tensor-memory kernel counts tokens in 32 bits, up to two chunks past the
+// end.
+constexpr int64_t kMaxTcSteps = int64_t(1) << 30;
 // The decay's gradient sums differences inside a segment: a bounded segment
 // bounds how many of them are added up.
 constexpr int64_t kGateSegment = 2048;
@@ -49,7 +54,7 @@ int check_dims(ssm_linattn_dims *d, int dtype, int64_t max_value) {
     return SSM_ERR_INVALID;
   int64_t rows = 0, n = 0, st = 0;
   if (__builtin_mul_overflow(d->batch, d->seqlen, &rows) ||
-      rows > kMaxElements)
+      rows > kMaxElements || d->seqlen > kMaxSteps)
     return SSM_ERR_INVALID;
   for (int64_t s : {d->q_stride, d->k_stride, d->v_stride, d->heads * d->dk})
     if (__builtin_mul_overflow(rows, s, &n) || n > kMaxElements)
@@ -109,7 +114,7 @@ Plan plan_fwd(const ssm_linattn_dims &d, Path path, int sms) {
   const int64_t all = d.batch * d.heads;
   // One block an SM: where the last round of blocks would leave over half of
   // the SMs idle, its heads are cut (4 x 8192 x 40 heads of 128: 550 us with
-  // 12 heads in a round of their own, %TAIL% with these cut).
+  // 12 heads in a round of their own, 359 us with these cut).
   auto cut_for = [&](int64_t heads) {
     cut(&pl, heads * (path == Path::kTc ? 1 : tiles), d.seqlen, sms, path,
         int64_t(1) << 40);
@@ -240,7 +245,7 @@ bool tc_rows(const void *q, int64_t stride, int64_t d) {
 bool tc_takes(const ssm_linattn_dims &d, int dtype, const void *q,
               const void *k, const void *v,
               std::initializer_list<const void *> dense) {
-  if (dtype != SSM_BF16 || d.dv > 128 || d.seqlen >= (int64_t(1) << 31) ||
+  if (dtype != SSM_BF16 || d.dv > 128 || d.seqlen > kMaxTcSteps ||
       d.batch >= (int64_t(1) << 31) || !tc_rows(q, d.q_stride, d.dk) ||
       !tc_rows(k, d.k_stride, d.dk) || !tc_rows(v, d.v_stride, d.dv) ||
       d.seqlen * d.q_stride >= (int64_t(1) << 38) ||
@@ -323,6 +328,16 @@ int run_tc(const LaParams &p, int n, bool exact, int device, cudaStream_t s) {
                     : launch_tc<128, 128, 1>(pp, n, s));
 }
 
+// Every token's rows of a tensor, from the first element to the last.
+ssm::Span rows_span(const void *at, const ssm_linattn_dims &d, int64_t stride,
+                    int64_t row, size_t esz) {
+  return {at, size_t((d.batch * d.seqlen - 1) * stride + row) * esz};
+}
+
+ssm::Span state_span(const float *at, const ssm_linattn_dims &d) {
+  return {at, size_t(d.batch * d.heads * d.dk * d.dv) * sizeof(float)};
+}
+
 bool check_floats(std::initializer_list<const float *> list) {
   for (const float *q : list)
     if (q && !aligned(q, 4)) return false;
@@ -347,9 +362,9 @@ LaParams common(const ssm_linattn_dims &d, const Plan &pl,
 
 template <typename T>
 void group_sum(const float *part, const ssm_linattn_dims &d, void *out,
-               cudaStream_t s) {
+               int sms, cudaStream_t s) {
   const int64_t n = d.batch * d.seqlen * d.groups * d.dk;
-  const int64_t grid = std::min<int64_t>(ceil_div(n, 256), 148 * 16);
+  const int64_t grid = std::min<int64_t>(ceil_div(n, 256), int64_t(sms) * 16);
   ssm::la::linattn_group_sum_kernel<T><<<unsigned(grid), 256, 0, s>>>(
       part, d.batch * d.seqlen, int(d.groups), int(d.heads / d.groups),
       int(d.dk), static_cast<T *>(out));
@@ -399,6 +414,19 @@ int ssm_linattn_fwd(int device, const void *q, const void *k, const void *v,
   if (!check_floats({head_log_decay, h0, h_last,
                      reinterpret_cast<const float *>(lengths)}))
     return SSM_ERR_ALIGN;
+  const int64_t G = dims.groups * dims.dk, H = dims.heads * dims.dv;
+  const ssm::Span out_y = rows_span(y, dims, H, H, esz),
+                  in_h = state_span(h0 == h_last ? nullptr : h0, dims),
+                  out_h = state_span(h_last, dims);
+  if (ssm::clash({out_y, out_h},
+                 {rows_span(q, dims, dims.q_stride, G, esz),
+                  rows_span(k, dims, dims.k_stride, G, esz),
+                  rows_span(v, dims, dims.v_stride, H, esz),
+                  rows_span(log_decay, dims, dims.heads, dims.heads, esz),
+                  {head_log_decay, size_t(dims.heads) * sizeof(float)},
+                  {lengths, size_t(dims.batch) * sizeof(int32_t)},
+                  in_h}))
+    return SSM_ERR_INVALID;
   int sms = 0;
   rc = ssm::device_ready(device, &sms);
   if (rc != SSM_OK) return rc;
@@ -453,6 +481,14 @@ int ssm_linattn_step(int device, const void *q, const void *k, const void *v,
   for (const void *a : {q, k, v, log_decay, static_cast<const void *>(y)})
     if (a && !aligned(a, esz)) return SSM_ERR_ALIGN;
   if (!check_floats({head_log_decay, state})) return SSM_ERR_ALIGN;
+  const int64_t G = dims.groups * dims.dk, H = dims.heads * dims.dv;
+  if (ssm::clash({state_span(state, dims), rows_span(y, dims, H, H, esz)},
+                 {rows_span(q, dims, dims.q_stride, G, esz),
+                  rows_span(k, dims, dims.k_stride, G, esz),
+                  rows_span(v, dims, dims.v_stride, H, esz),
+                  rows_span(log_decay, dims, dims.heads, dims.heads, esz),
+                  {head_log_decay, size_t(dims.heads) * sizeof(float)}}))
+    return SSM_ERR_INVALID;
   int sms = 0;
   rc = ssm::device_ready(device, &sms);
   if (rc != SSM_OK) return rc;
@@ -509,6 +545,26 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
   if (!check_floats({head_log_decay, h0, dh_last, dhead_log_decay, dh0,
                      reinterpret_cast<const float *>(lengths)}))
     return SSM_ERR_ALIGN;
+  const int H = int(dims.heads), G = int(dims.groups), K = int(dims.dk),
+            V = int(dims.dv);
+  const int64_t dy_stride = int64_t(H) * V;
+  const size_t heads_bytes = size_t(H) * sizeof(float);
+  const int64_t qk = int64_t(G) * K;
+  if (ssm::clash({rows_span(dq, dims, qk, qk, esz),
+                  rows_span(dk, dims, qk, qk, esz),
+                  rows_span(dv, dims, dy_stride, dy_stride, esz),
+                  rows_span(dlog_decay, dims, H, H, esz),
+                  {dhead_log_decay, heads_bytes}, state_span(dh0, dims)},
+                 {rows_span(q, dims, dims.q_stride, qk, esz),
+                  rows_span(k, dims, dims.k_stride, qk, esz),
+                  rows_span(v, dims, dims.v_stride, dy_stride, esz),
+                  rows_span(log_decay, dims, H, H, esz),
+                  {head_log_decay, heads_bytes},
+                  {lengths, size_t(dims.batch) * sizeof(int32_t)},
+                  state_span(h0, dims),
+                  rows_span(dy, dims, dy_stride, dy_stride, esz),
+                  state_span(dh_last, dims)}))
+    return SSM_ERR_INVALID;
   int sms = 0;
   rc = ssm::device_ready(device, &sms);
   if (rc != SSM_OK) return rc;
@@ -529,10 +585,7 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
   auto at = [&](size_t off) { return reinterpret_cast<float *>(ws + off); };
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
 
-  const int H = int(dims.heads), G = int(dims.groups), K = int(dims.dk),
-            V = int(dims.dv);
   const bool shared = G != H;
-  const int64_t dy_stride = int64_t(H) * V;
   LaJob jq{}, jk{}, jv{};
   // dq: query dy, key v, value k
   jq.q = dy; jq.q_stride = dy_stride; jq.q_heads = H;
@@ -597,11 +650,11 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
 
   if (shared) {
     if (dtype == SSM_F32) {
-      group_sum<float>(at(pl.part_dq), dims, dq, s);
-      group_sum<float>(at(pl.part_dk), dims, dk, s);
+      group_sum<float>(at(pl.part_dq), dims, dq, sms, s);
+      group_sum<float>(at(pl.part_dk), dims, dk, sms, s);
     } else {
-      group_sum<bf16>(at(pl.part_dq), dims, dq, s);
-      group_sum<bf16>(at(pl.part_dk), dims, dk, s);
+      group_sum<bf16>(at(pl.part_dq), dims, dq, sms, s);
+      group_sum<bf16>(at(pl.part_dk), dims, dk, sms, s);
     }
     if (cudaGetLastError() != cudaSuccess) return SSM_ERR_CUDA;
   }

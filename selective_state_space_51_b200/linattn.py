@@ -122,7 +122,9 @@ class LinearAttention:
             raise dtype_error()
         G, dk = sq[-2:]
         H, dv = sv[-2:]
-        if sv[:-2] != sq[:-2] or G == 0 or H % G:
+        if 0 in sq or 0 in sv:
+            raise ValueError("q, k and v must not be empty")
+        if sv[:-2] != sq[:-2] or H % G:
             raise ValueError("v must have q's tokens, and a multiple of its "
                              "heads")
         rows = self._rows

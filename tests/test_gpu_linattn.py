@@ -239,6 +239,15 @@ def test_restarts(attn, dtype, value):
 
 
 @pytest.mark.parametrize("dtype", sorted(TYPES))
+def test_a_restart_has_no_decay_gradient(attn, dtype):
+    c = Case(dtype, 2, 300, 4, 2, 32, 16, gate="token")
+    at = [0, 5, 63, 64, 128, 299]
+    c.log_decay[:, at] = -np.inf
+    g = c.run_back(attn)["dlog_decay"]
+    assert not g[:, at].any() and bool(g.isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
 def test_decay_extremes(attn, dtype):
     """Strong decays next to none: the differences of the sums stay exact."""
     c = Case(dtype, 1, 256, 2, 2, 16, 16, gate="token")
@@ -399,6 +408,57 @@ def test_captured_calls_replay(attn):
             assert torch.equal(c_state, state)
 
 
+def test_raw_streams(attn):
+    c = Case("bf16", 1, 300, 2, 2, 32, 32)
+    y, h = c.run(attn)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for s in (0, side.cuda_stream, side):
+        y2, h2 = c.run(attn, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and torch.equal(h, h2)
+
+
+FIRST = """
+import torch
+import selective_state_space_51_b200 as S
+attn, norm = S.LinearAttention(), S.LayerNorm()
+q = torch.randn(1, 300, 2, 32, device="cuda", dtype=torch.%s)
+x = torch.randn(64, 96, device="cuda")
+w = torch.ones(96, device="cuda")
+state = torch.zeros(1, 2, 32, 32, device="cuda")
+
+def calls():
+    y, h = attn(q, q, q)
+    g = attn.backward(q, q, q, q)
+    state.zero_()
+    s = attn.step(q[:, 0], q[:, 0], q[:, 0], state)
+    f = norm(x, w)
+    b = norm.backward(x, x, f["mean"], f["rstd"], w)
+    return [y, h, s, f["y"], b["dx"], b["dweight"]] + [
+        g[n] for n in ("dq", "dk", "dv", "dh0")]
+
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    got = calls()
+graph.replay()
+torch.cuda.synchronize()
+for a, b in zip(got, calls()):
+    assert torch.equal(a, b)
+print("same")
+"""
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_the_first_call_of_a_process_is_captured(dtype):
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", FIRST % dtype], text=True,
+                       capture_output=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
 def test_far_tokens(attn):
     """Offsets past 2^31 elements: the last sequence of a batch whose rows
     lie far apart gives what it gives alone."""
@@ -433,6 +493,13 @@ def test_refused_tensors(attn):
         attn(q.half(), q.half(), v.half())
     with pytest.raises(ValueError):
         attn.backward(q, q, v, None)
+    for empty in (dict(q=q[..., :0], k=q[..., :0]), dict(q=q[:, :, :0]),
+                  dict(v=v[:, :, :0]), dict(q=q[:, :0], k=q[:, :0],
+                                            v=v[:, :0])):
+        with pytest.raises(ValueError):
+            attn(**{**ok, **empty})
+    with pytest.raises(S.SsmScanError):
+        attn(**ok, y=v)
     with pytest.raises(S.SsmScanError) as e:
         wide = torch.zeros(1, 4, 1, 130, device="cuda")
         attn(wide, wide, torch.zeros(1, 4, 1, 8, device="cuda"))

@@ -155,6 +155,93 @@ def test_norm_refusals(lib):
         assert call(lib, weight=P + 2) == S.SSM_ERR_ALIGN
 
 
+def far(names, first=1 << 30, step=1 << 24):
+    """Addresses of buffers that lie apart."""
+    return {n: first + i * step for i, n in enumerate(names)}
+
+
+FWD = ("q", "k", "v", "log_decay", "head", "lengths", "h0", "y", "h_last",
+       "ws")
+BWD = ("q", "k", "v", "log_decay", "head", "lengths", "h0", "dy", "dh_last",
+       "dq", "dk", "dv", "dlog_decay", "dhead", "dh0", "ws")
+NORM = ("x", "residual", "weight", "bias", "y", "sum", "mean", "rstd")
+NORM_BACK = ("dy", "x", "mean", "rstd", "weight", "dsum", "dx", "dweight",
+             "dbias", "ws")
+
+
+def passes(rc):
+    """A call whose arguments are accepted gets as far as the device."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present: these addresses are not its own")
+    assert rc in (S.SSM_ERR_CUDA, S.SSM_ERR_ARCH)
+
+
+@pytest.mark.parametrize("out", ["y", "h_last"])
+@pytest.mark.parametrize("other", ["q", "k", "v", "log_decay", "head",
+                                   "lengths", "h0", "y"])
+def test_forward_outputs_lie_apart(lib, out, other):
+    a = far(FWD)
+    if (out, other) == ("y", "y"):
+        return passes(fwd(lib, **a))
+    if (out, other) == ("h_last", "h0"):
+        passes(fwd(lib, **{**a, out: a[other]}))     # in place
+        assert fwd(lib, **{**a, out: a[other] + 8}) == S.SSM_ERR_INVALID
+    else:
+        assert fwd(lib, **{**a, out: a[other]}) == S.SSM_ERR_INVALID
+
+
+def test_strided_rows_count_to_their_last_element(lib):
+    a, d = far(FWD), dims(q_stride=100)   # 2 x 8 tokens
+    end = a["q"] + (15 * 100 + 32) * 4
+    assert fwd(lib, d, **{**a, "y": end - 8}) == S.SSM_ERR_INVALID
+    passes(fwd(lib, d, **{**a, "y": end}))
+
+
+@pytest.mark.parametrize("out", BWD[9:15])
+@pytest.mark.parametrize("other", BWD[:15])
+def test_backward_outputs_lie_apart(lib, out, other):
+    a = far(BWD)
+    if out == other:
+        return passes(bwd(lib, **a))
+    assert bwd(lib, **{**a, out: a[other]}) == S.SSM_ERR_INVALID
+
+
+@pytest.mark.parametrize("other", ["q", "k", "v", "log_decay", "head", "y"])
+def test_step_outputs_lie_apart(lib, other):
+    a = far(("q", "k", "v", "log_decay", "head", "state", "y"))
+    assert step(lib, **{**a, "state": a[other]}) == S.SSM_ERR_INVALID
+    if other != "y":
+        assert step(lib, **{**a, "y": a[other]}) == S.SSM_ERR_INVALID
+    passes(step(lib, **a))
+
+
+def test_norm_in_place_or_apart(lib):
+    a = far(NORM)
+    for out in ("y", "sum"):
+        for other in ("x", "residual"):
+            assert norm(lib, **{**a, out: a[other] + 16}) == S.SSM_ERR_INVALID
+        for other in ("weight", "mean"):
+            assert norm(lib, **{**a, out: a[other]}) == S.SSM_ERR_INVALID
+    assert norm(lib, **{**a, "sum": a["y"]}) == S.SSM_ERR_INVALID
+    assert norm(lib, **{**a, "mean": a["x"]}) == S.SSM_ERR_INVALID
+    b = far(NORM_BACK)
+    for other in ("x", "dy", "dsum"):
+        assert norm_back(lib, **{**b, "dx": b[other] + 16}) == \
+            S.SSM_ERR_INVALID
+        assert norm_back(lib, **{**b, "dbias": b[other]}) == S.SSM_ERR_INVALID
+    assert norm_back(lib, **{**b, "dweight": b["dbias"]}) == S.SSM_ERR_INVALID
+    for out, other in (("y", "x"), ("y", "residual"), ("sum", "x")):
+        passes(norm(lib, **{**a, out: a[other]}))
+    for other in ("x", "dy", "dsum"):
+        passes(norm_back(lib, **{**b, "dx": b[other]}))
+
+
+def test_more_steps_than_a_device_holds(lib):
+    d = dims(batch=1, seqlen=1 << 37, heads=1, groups=1, dk=1, dv=1)
+    assert fwd(lib, d) == bwd(lib, d) == S.SSM_ERR_INVALID
+
+
 def test_without_a_gpu_the_calls_fail_cleanly(lib):
     import torch
     if torch.cuda.is_available():
