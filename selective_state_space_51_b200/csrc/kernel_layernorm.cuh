@@ -136,6 +136,17 @@ __device__ __forceinline__ void row_sum2(float &a, float &b, int wpr,
   }
 }
 
+// Where a thread's parameters wait in shared memory rather than registers, of
+// which its elements take too many there: forward weight and bias, backward
+// the weight (65536 x 1024 bfloat16, backward: 126 us with it in registers,
+// 104 so; 32768 x 2560: 139 either way).
+__host__ __device__ constexpr bool shared_params(int v, int n) {
+  return v == 8 && n > 2;
+}
+__host__ __device__ constexpr bool shared_weight(int v, int g) {
+  return v == 8 && g == 32;
+}
+
 // Blocks stay for many rows: a thread's parameters are read once, and the next
 // row is on its way while this one is reduced and written.
 template <typename T, int V, int N, int G>
@@ -147,7 +158,16 @@ __global__ void __launch_bounds__(512)
   const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes;
   const float inv = 1.0f / float(p.dim);
   const int64_t steps = (p.rows + per - 1) / per;
-  float w[N][V], b[N][V];
+  constexpr bool SH = shared_params(V, N);
+  extern __shared__ __align__(16) float par[];
+  float w[SH ? 1 : N][V], b[SH ? 1 : N][V];
+  if constexpr (SH) {
+    for (int c = threadIdx.x; c < p.dim; c += blockDim.x) {
+      par[c] = p.weight ? p.weight[c] : 1.0f;
+      par[p.dim + c] = p.bias ? p.bias[c] : 0.0f;
+    }
+    __syncthreads();
+  } else
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int c = (i * lanes + lane) * V;
@@ -222,6 +242,18 @@ __global__ void __launch_bounds__(512)
     for (int i = 0; i < N; ++i) {
       const int c = (i * lanes + lane) * V;
       if (in && c < p.dim) {
+        if constexpr (SH) {
+#pragma unroll
+          for (int j = 0; j < V; j += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(par + c + j);
+            const float4 e =
+                *reinterpret_cast<const float4 *>(par + p.dim + c + j);
+            f[i][j] = fmaf(f[i][j] * rstd, a.x, e.x);
+            f[i][j + 1] = fmaf(f[i][j + 1] * rstd, a.y, e.y);
+            f[i][j + 2] = fmaf(f[i][j + 2] * rstd, a.z, e.z);
+            f[i][j + 3] = fmaf(f[i][j + 3] * rstd, a.w, e.w);
+          }
+        } else
 #pragma unroll
         for (int j = 0; j < V; ++j)
           f[i][j] = fmaf(f[i][j] * rstd, w[i][j], b[i][j]);
@@ -240,8 +272,9 @@ template <typename T, int V, int N, int G>
 __global__ void __launch_bounds__(512, V == 1 && N <= 4 ? 2 : 1)
     layernorm_bwd_kernel(const __grid_constant__ NormParams p) {
   constexpr bool FOLD = N * V <= 8;
+  constexpr bool LEAN = shared_weight(V, G);
   __shared__ float2 red[64];
-  extern __shared__ float cols[];  // [per - 1, 2, dim] at the end
+  extern __shared__ __align__(16) float cols[];  // [per - 1, 2, dim] at the end
   const int lanes = G < 32 ? G : 32 * p.wpr;
   const int per = blockDim.x / lanes;
   const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes;
@@ -253,13 +286,20 @@ __global__ void __launch_bounds__(512, V == 1 && N <= 4 ? 2 : 1)
 #pragma unroll
     for (int j = 0; j < V; ++j)
       dw[i][j] = db[i][j] = dw2[i][j] = db2[i][j] = 0.0f;
-  float w[N][V];
+  float w[LEAN ? 1 : N][V];
+  float *ws = cols + (p.part ? (per - 1) * 2 * p.dim : 0);
+  if constexpr (LEAN) {
+    for (int c = threadIdx.x; c < p.dim; c += blockDim.x)
+      ws[c] = p.weight ? p.weight[c] : 1.0f;
+    __syncthreads();
+  } else {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int c = (i * lanes + lane) * V;
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * lanes + lane) * V;
 #pragma unroll
-    for (int j = 0; j < V; ++j) w[i][j] = 1.0f;
-    if (c < p.dim && p.weight) load_param<V>(p.weight + c, w[i]);
+      for (int j = 0; j < V; ++j) w[i][j] = 1.0f;
+      if (c < p.dim && p.weight) load_param<V>(p.weight + c, w[i]);
+    }
   }
   Raw<T, V> nx[N], ng[N];
   float nmean = 0.0f, nrstd = 0.0f;
@@ -302,13 +342,25 @@ __global__ void __launch_bounds__(512, V == 1 && N <= 4 ? 2 : 1)
     for (int i = 0; i < N; ++i) {
       const int c = (i * lanes + lane) * V;
       const bool live = c < p.dim;
+      float wi[V];
+      if constexpr (LEAN) {
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+          const float4 v =
+              *reinterpret_cast<const float4 *>(ws + (live ? c + j : 0));
+          wi[j] = v.x; wi[j + 1] = v.y; wi[j + 2] = v.z; wi[j + 3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) wi[j] = w[i][j];
+      }
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         x[i][j] = live ? (nx[i].at(j) - mean) * rstd : 0.0f;
         g[i][j] = ng[i].at(j);
         dw[i][j] = fmaf(g[i][j], x[i][j], dw[i][j]);
         db[i][j] += g[i][j];
-        g[i][j] *= w[i][j];
+        g[i][j] *= wi[j];
         su += g[i][j];
         sux = fmaf(g[i][j], x[i][j], sux);
       }

@@ -15,6 +15,9 @@ using ssm::aligned;
 using ssm::NormParams;
 using bf16 = __nv_bfloat16;
 
+// Dynamic shared memory that needs no permission beside the kernels' own.
+constexpr size_t kSmallSmem = 47 * 1024;
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // How a row is spread: G lanes (short rows) or wpr warps, n groups a thread.
@@ -23,21 +26,38 @@ struct Shape {
   int threads = 256, per = 1;  // of a block; rows of a block
 };
 
-// A thread holds at most 2 groups of 16 bytes, or 8 single elements (4 where
-// bfloat16 ones are normed): more of them cost residency (registers) than they
-// save barriers, fewer the reverse (32768 x 511 float32, backward: 158 us for
-// twice the bytes with 8, 182 with 4, 236 with 2; 511 bfloat16, forward: 532
-// us with 4, 828 with 8). Rows wider than 16 warps' worth of that (the launch
-// bound) take more.
-Shape shape_of(int dim, int v, int singles) {
+// Groups of a thread, for rows of more than 16 of them. Single elements: at
+// most 8 (4 where bfloat16 ones are normed): more of them cost residency
+// (registers) than they save barriers, fewer the reverse (32768 x 511 float32,
+// backward: 158 us for twice the bytes with 8, 182 with 4, 236 with 2; 511
+// bfloat16, forward: 532 us with 4, 828 with 8). 16-byte groups: 2 to `most`
+// (4; in the backward pass, which keeps two sums for every element, 2, and 3 of
+// float32), as many as leave the fewest lanes idle, and of these the most, for fewer
+// warps have to meet then (bfloat16 forward, with residual: 131072 x 768 174 us
+// with 2, 130 with 3 and no barrier; 16384 x 5120 175 us with 2, 118 with 4;
+// 32768 x 2560 127 us with 2, 142 with 4 and idle lanes; 16384 x 4096 98 us
+// with 2, 102 with 4; float32 backward: 65536 x 768 153 us with 2, 129 with 3;
+// 32768 x 1024 94 us with 2, 132 with 4).
+Shape shape_of(int dim, int v, int most) {
   Shape s;
   const int nv = int(ceil_div(dim, v));
   if (nv <= 16) {
     s.g = nv <= 4 ? 4 : nv <= 8 ? 8 : 16;
-  } else {
-    const int most = std::max<int>(v == 1 ? singles : 2, int(ceil_div(nv, 512)));
+  } else if (v == 1) {
+    // (rows wider than 16 warps' worth of that, the launch bound, take more)
+    most = std::max<int>(most, int(ceil_div(nv, 512)));
     s.wpr = int(ceil_div(nv, 32 * most));
     s.n = int(ceil_div(nv, 32 * s.wpr));
+  } else {
+    int idle = 1 << 30;
+    for (int n = nv <= 32 ? 1 : 2; n <= std::max(most, int(ceil_div(nv, 512)));
+         ++n) {
+      const int wpr = int(ceil_div(nv, 32 * n)), left = 32 * n * wpr - nv;
+      if (wpr > 16 || left > idle) continue;
+      idle = left;
+      s.wpr = wpr;
+      s.n = n;
+    }
   }
   const int lanes = s.g < 32 ? s.g : 32 * s.wpr;
   s.per = std::max(1, 256 / lanes);
@@ -53,7 +73,7 @@ int parts_of(const Shape &s, int64_t rows, int sms) {
 }
 
 // Blocks of `threads` that an SM holds at once.
-int resident(const void *kern, int threads, size_t smem = 0) {
+int resident(const void *kern, int threads, size_t smem) {
   int n = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) !=
           cudaSuccess ||
@@ -68,10 +88,18 @@ template <typename T, int V, int N, int G>
 int launch_fwd(const NormParams &p, const Shape &s, int sms, cudaStream_t st) {
   const int64_t steps = ceil_div(p.rows, s.per);
   auto kern = ssm::norm::layernorm_fwd_kernel<T, V, N, G>;
+  const size_t smem =
+      ssm::norm::shared_params(V, N) ? size_t(p.dim) * 2 * sizeof(float) : 0;
+  if (smem > kSmallSmem &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           int(smem)) != cudaSuccess) {
+    cudaGetLastError();
+    return SSM_ERR_CUDA;
+  }
   const int64_t grid = std::min<int64_t>(
       steps, int64_t(sms) * resident(reinterpret_cast<const void *>(kern),
-                                     s.threads));
-  kern<<<unsigned(grid), s.threads, 0, st>>>(p);
+                                     s.threads, smem));
+  kern<<<unsigned(grid), s.threads, smem, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
 
@@ -79,8 +107,9 @@ template <typename T, int V, int N, int G>
 int launch_bwd(NormParams p, const Shape &s, int sms, cudaStream_t st) {
   auto kern = ssm::norm::layernorm_bwd_kernel<T, V, N, G>;
   const size_t smem =
-      p.part ? size_t(s.per - 1) * 2 * p.dim * sizeof(float) : 0;
-  if (smem > 48 * 1024 &&
+      (size_t(p.part ? (s.per - 1) * 2 : 0) + (ssm::norm::shared_weight(V, G) ? 1 : 0)) *
+      p.dim * sizeof(float);
+  if (smem > kSmallSmem &&
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            int(smem)) != cudaSuccess) {
     cudaGetLastError();
@@ -110,7 +139,7 @@ int pick(const NormParams &p, const Shape &s, int sms, cudaStream_t st) {
   if (s.g == 16) return launch<T, V, BWD, 1, 16>(p, s, sms, st);
   if (s.n == 1) return launch<T, V, BWD, 1, 32>(p, s, sms, st);
   if (s.n == 2) return launch<T, V, BWD, 2, 32>(p, s, sms, st);
-  if constexpr (V < 8) {
+  if constexpr (V < 8 || !BWD) {
     if (s.n <= 3) return launch<T, V, BWD, 3, 32>(p, s, sms, st);
     if (s.n <= 4) return launch<T, V, BWD, 4, 32>(p, s, sms, st);
   }
@@ -155,10 +184,9 @@ bool wide_rows(int64_t dim, size_t esz,
   return true;
 }
 
-int width(bool wide, size_t esz) { return wide ? int(16 / esz) : 1; }
-
 Shape row_shape(int64_t dim, bool wide, size_t esz, bool bwd) {
-  return shape_of(int(dim), width(wide, esz), bwd || esz == 4 ? 8 : 4);
+  if (!wide) return shape_of(int(dim), 1, bwd || esz == 4 ? 8 : 4);
+  return shape_of(int(dim), int(16 / esz), bwd ? (esz == 4 ? 3 : 2) : 4);
 }
 
 }  // namespace

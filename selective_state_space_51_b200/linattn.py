@@ -182,7 +182,7 @@ class LinearAttention:
                 h0, y, h_last, want_last, dims, code):
         torch = self._torch
         if y is None:
-            y = torch.empty(v.shape, dtype=q.dtype, device=self.device)
+            y = torch.empty_like(v, memory_format=torch.contiguous_format)
         if h_last is None and want_last:
             h_last = torch.empty((dims[0], dims[2], dims[4], dims[5]),
                                  dtype=torch.float32, device=self.device)
@@ -213,7 +213,7 @@ class LinearAttention:
               dims, code):
         torch = self._torch
         if y is None:
-            y = torch.empty(v.shape, dtype=q.dtype, device=self.device)
+            y = torch.empty_like(v, memory_format=torch.contiguous_format)
         _check(self._lib.ssm_linattn_step(
             self.device.index, q.data_ptr(), k.data_ptr(), v.data_ptr(),
             ptr(log_decay), ptr(head_log_decay), scale, state.data_ptr(),

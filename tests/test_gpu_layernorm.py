@@ -117,6 +117,21 @@ def test_widths(norm, dtype, dim):
 
 
 @pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("dim", [264, 768, 1280, 1792, 2304, 4104, 6144, 6152,
+                                 8184])
+def test_groups_a_thread(norm, dtype, dim):
+    """Two to four 16-byte groups a thread, with and without idle lanes, and
+    parameters beyond the small shared memory."""
+    check(norm, dtype, 37, dim, True, True)
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("dim", [768, 2304])
+def test_many_rows_a_block(norm, dtype, dim):
+    check(norm, dtype, 3000, dim, True, True)
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
 @pytest.mark.parametrize("rows", [1, 2, 3, 255, 5000])
 @pytest.mark.parametrize("dim", [24, 33, 320])
 def test_rows(norm, dtype, rows, dim):
