@@ -19,6 +19,11 @@
 // Layout. A row belongs to G lanes of a warp (G < 32, short rows) or to
 // `wpr` whole warps; a thread holds N groups of V consecutive elements (V: 16
 // bytes where rows allow it, else 1), group i at column (i * lanes + lane) V.
+//
+// bfloat16 with residual, 32768 x 2560: 127 us (5.3 TB/s, 0.81 of the copy
+// rate), backward with dsum 139 us (0.74: two sums an element hold registers);
+// 131072 x 768: 130 us (0.95), backward 170. Single elements (32768 x 511
+// float32, backward): 68 us of 31, bound by the number of loads.
 #pragma once
 
 #include <cuda_bf16.h>

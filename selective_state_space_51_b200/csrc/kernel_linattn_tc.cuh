@@ -33,6 +33,12 @@
 // e^{c_i - c_r} e^{c_r - c_j}, r the last step of j's block: both factors are
 // at most 1 for decays (no overflow), so a block costs one exponential a row
 // and two products an element. On the diagonal it is formed directly.
+//
+// 148 heads x 8192 steps of (128, 128): 288 us, 4.3 TB/s (0.66 of the copy
+// rate); bound by a chunk's chain (state, its copy, products, weighted values,
+// update: 4.5 us), with 52% of the issue slots and 38% of the tensor pipe busy.
+// Loops unrolled past the instruction cache: 370 us; eight warps doing all of
+// it in turn, 160 heads: 1.1 ms.
 #pragma once
 
 #include "kernel_linattn.cuh"
@@ -161,7 +167,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_live = int(n_left);
   const int64_t idle_low = seg_low + int64_t(n_live) * kChunk;
   const int low0 = int(rev ? idle_low - kChunk : seg_low);
-  auto low = [&](int it) { return rev ? low0 - it * kChunk : low0 + it * kChunk; };
+  auto low = [&](int it) {
+    return rev ? low0 - it * kChunk : low0 + it * kChunk;
+  };
   // the chunk in which the sequence ends before its rows do, or -1
   const int ragged =
       len < L && len % kChunk != 0 && n_live > 0

@@ -32,8 +32,8 @@ struct Shape {
 // backward: 158 us for twice the bytes with 8, 182 with 4, 236 with 2; 511
 // bfloat16, forward: 532 us with 4, 828 with 8). 16-byte groups: 2 to `most`
 // (4; in the backward pass, which keeps two sums for every element, 2, and 3 of
-// float32), as many as leave the fewest lanes idle, and of these the most, for fewer
-// warps have to meet then (bfloat16 forward, with residual: 131072 x 768 174 us
+// float32), as many as leave the fewest lanes idle, and of these the most, for
+// fewer warps have to meet then (bfloat16 forward, with residual: 131072 x 768 174 us
 // with 2, 130 with 3 and no barrier; 16384 x 5120 175 us with 2, 118 with 4;
 // 32768 x 2560 127 us with 2, 142 with 4 and idle lanes; 16384 x 4096 98 us
 // with 2, 102 with 4; float32 backward: 65536 x 768 153 us with 2, 129 with 3;
@@ -107,7 +107,8 @@ template <typename T, int V, int N, int G>
 int launch_bwd(NormParams p, const Shape &s, int sms, cudaStream_t st) {
   auto kern = ssm::norm::layernorm_bwd_kernel<T, V, N, G>;
   const size_t smem =
-      (size_t(p.part ? (s.per - 1) * 2 : 0) + (ssm::norm::shared_weight(V, G) ? 1 : 0)) *
+      (size_t(p.part ? (s.per - 1) * 2 : 0) +
+       (ssm::norm::shared_weight(V, G) ? 1 : 0)) *
       p.dim * sizeof(float);
   if (smem > kSmallSmem &&
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -205,7 +206,8 @@ int ssm_layernorm_workspace(int device, int64_t rows, int64_t dim, int dtype,
   const size_t esz = dtype == SSM_F32 ? 4 : 2;
   int parts = parts_of(row_shape(dim, false, esz, true), rows, sms);
   if (dim * esz % 16 == 0)
-    parts = std::max(parts, parts_of(row_shape(dim, true, esz, true), rows, sms));
+    parts = std::max(parts,
+                     parts_of(row_shape(dim, true, esz, true), rows, sms));
   *bytes = size_t(parts) * 2 * dim * sizeof(float);
   return SSM_OK;
 }
