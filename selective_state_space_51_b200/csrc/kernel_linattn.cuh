@@ -31,8 +31,8 @@
 // Bound by the tensor pipe's mma.sync rate and by what feeds it: six products
 // for float32 operands, at 40% of the pipe's cycles. 64 steps a chunk and 64
 // value columns a block leave room for two blocks an SM (one with three planes
-// of 128-wide keys). float32, 64 x up to 512 steps, 8 heads of 64: 190 us, the
-// bytes alone 42; backward, 3 x 1000 steps, 6 heads of 48 x 77: 187 us with
+// of 128-wide keys). float32, 64 x up to 512 steps, 8 heads of 64: 194 us, the
+// bytes alone 42; backward, 3 x 1000 steps, 6 heads of 48 x 77: 188 us with
 // its ten short launches.
 #pragma once
 
@@ -723,8 +723,11 @@ __global__ void __launch_bounds__(kThreads, MINB)
       }
     }
 
-    // the next chunk's decays, by a warp whose rows have the fewest scores
-    ready = ch + 1 < chunks;
+    // the next chunk's decays, by a warp whose rows have the fewest scores;
+    // where an SM holds one block only, for another would fill the wait (2 x
+    // 4096 steps, 16 heads of 128, float32: 641 us without, 620 so; 64 x 512
+    // steps, 8 heads of 64, two blocks an SM: 199 without, 204 so)
+    ready = MINB == 1 && ch + 1 < chunks;
     if (warp == 0 && ready)
       load_gates<T>(gates[(ch + 1) & 1], p, rows_of(ch + 1), b, h,
                     job.reverse);
