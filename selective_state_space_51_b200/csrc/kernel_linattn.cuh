@@ -876,13 +876,17 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
 //   dg_t = <a_t S_{t-1}, G_t> = dg_{t+1} + q_t . dq_t - k_t . dk_t,
 // summed backwards inside each segment from its end, where the product of the
 // state and its gradient is formed from the two passes' segment states: the
-// differences are then never summed over more than one segment. One block
-// per (sequence, head, segment).
+// differences are then never summed over more than one segment. A step that
+// starts the state anew has no gradient, and the sum starts from 0 there: the
+// differences behind it cancel in exact arithmetic only, and what rounding
+// leaves of them is not the business of the steps in front. One block per
+// (sequence, head, segment).
 template <typename T>
 __global__ void __launch_bounds__(256)
     linattn_gate_kernel(const __grid_constant__ LaGateParams p) {
   __shared__ float red[8];
   __shared__ float warp_tot[8];
+  __shared__ bool warp_anew[8];
   const int64_t x = blockIdx.x;
   const int seg = int(x % p.nseg);
   const int64_t bh = x / p.nseg;
@@ -958,30 +962,53 @@ __global__ void __launch_bounds__(256)
       for (int j = 0; j < kRun; ++j)
         if (in(j)) v[j] += q[at - j] - r[at - j];
     }
+    // sums since the last restart behind each token; `anew`: there is one in
+    // this thread's tokens so far (bits), its warp's, the block's
+    uint32_t anew = 0u;
 #pragma unroll
-    for (int j = 1; j < kRun; ++j) v[j] += v[j - 1];
+    for (int j = 0; j < kRun; ++j) {
+      const bool starts = in(j) && log2_of(to_f(g[j])) < -126.0;
+      anew |= uint32_t(starts) << j;
+      v[j] = starts ? 0.0f : j ? v[j] + v[j - 1] : v[j];
+    }
     float sum = v[kRun - 1];
+    int any = anew != 0u;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const float o = __shfl_up_sync(0xffffffffu, sum, d);
-      if (lane >= d) sum += o;
+      const int oa = __shfl_up_sync(0xffffffffu, any, d);
+      if (lane >= d && !any) {
+        sum += o;
+        any = oa;
+      }
     }
-    if (lane == 31) warp_tot[warp] = sum;
+    if (lane == 31) {
+      warp_tot[warp] = sum;
+      warp_anew[warp] = any;
+    }
     // what lies behind this thread's tokens in its warp
     float before = __shfl_up_sync(0xffffffffu, sum, 1);
-    if (lane == 0) before = 0.0f;
+    int cut = __shfl_up_sync(0xffffffffu, any, 1);
+    if (lane == 0) {
+      before = 0.0f;
+      cut = 0;
+    }
     __syncthreads();
-    before += carry;
-    for (int w = 0; w < warp; ++w) before += warp_tot[w];
-    for (int w = 0; w < 8; ++w) carry += warp_tot[w];
+    float behind = carry;
+    for (int w = 0; w < 8; ++w) {
+      if (w == warp && !cut) before += behind;
+      behind = warp_anew[w] ? warp_tot[w] : behind + warp_tot[w];
+    }
+    carry = behind;
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
       const int64_t t = last - j;
       if (t >= t0 && t < L) {
         // (a step that starts the state anew does not depend on its decay)
-        const bool live = t < len && !(log2_of(to_f(g[j])) < -126.0);
-        const float out = live ? before + v[j] : 0.0f;
+        const bool live = t < len && !(anew >> j & 1u);
+        const bool whole = (anew & ((2u << j) - 1u)) == 0u;
+        const float out = live ? (whole ? before + v[j] : v[j]) : 0.0f;
         if (p.dlog_decay)
           static_cast<T *>(p.dlog_decay)[(b * L + t) * p.heads + h] = T(out);
         part += out;

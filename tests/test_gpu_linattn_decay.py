@@ -1,0 +1,70 @@
+"""The log decay's gradient over long sums and across restarts, as a whole
+(per head), within the bounds of decay_bound."""
+import numpy as np
+import pytest
+import torch
+
+import decay_bound as D
+import mixer_oracle as M
+import selective_state_space_51_b200 as S
+from test_gpu_linattn import Case, host
+
+pytestmark = pytest.mark.gpu
+
+# activation type, decay: the pass's kernel and planes
+PATHS = {"f32": ("f32", "both", "planes3"),
+         "bf16_head": ("bf16", "both", "planes3"),
+         "bf16_token": ("bf16", "token", "planes2")}
+
+
+@pytest.fixture(scope="module")
+def attn():
+    return S.LinearAttention(0)
+
+
+def reference(c):
+    return M.backward(c.q, c.k, c.v, c.g, c.scale, c.dy, c.h0, c.dh,
+                      c.lengths)
+
+
+@pytest.mark.parametrize("path", sorted(PATHS))
+@pytest.mark.parametrize("at", [1, 7, 700, 1000, 1023, 1024, 1499])
+def test_nothing_crosses_a_restart(attn, path, at):
+    """No gradient in front of a restart when all that is differentiated lies
+    behind it: exactly 0, wherever it falls."""
+    dtype, gate, _ = PATHS[path]
+    c = Case(dtype, 2, 1500, 2, 2, 64, 64, gate=gate, state=False)
+    c.log_decay[:, at] = -np.inf
+    c.dy[:, :at] = 0.0
+    c.dy *= 64.0
+    g = c.run_back(attn)
+    for n in ("dq", "dk", "dv", "dlog_decay"):
+        assert not g[n][:, :at].any(), n
+    assert not g["dlog_decay"][:, at].any()
+    assert g["dlog_decay"][:, at + 1:].any() or at == 1499
+    assert attn.sync_status() == S.SSM_OK
+
+
+@pytest.mark.parametrize("path", sorted(PATHS))
+def test_packed_documents_keep_their_own_scale(attn, path):
+    """Documents of one sequence whose gradients differ by 2^20: each within
+    the bound of its own size."""
+    dtype, gate, planes = PATHS[path]
+    c = Case(dtype, 1, 1700, 2, 2, 32, 32, gate=gate, state=False)
+    starts = [0, 333, 900, 1500, 1700]
+    size = [1.0, 2.0 ** 20, 1.0, 2.0 ** 20]
+    for i, s in zip(starts[1:], size):
+        c.log_decay[:, i % 1700] = -np.inf
+    for i, j, s in zip(starts, starts[1:], size):
+        c.dy[:, i:j] *= s
+    ref = reference(c)
+    got = host(c.run_back(attn)["dlog_decay"])
+    m = np.sqrt(((c.q * ref["dq"]) ** 2).sum(-1)
+                + ((c.k * ref["dk"]) ** 2).sum(-1))
+    for i, j in zip(starts, starts[1:]):
+        part = slice(i, j)
+        off = D.rms(got[:, part] - ref["dg"][:, part])
+        tol = 4 * D.DELTA[planes] * D.rms(m[:, part]) * np.sqrt(j - i) \
+            + (4 * 2.0 ** -22 + M.U[dtype]) * D.rms(ref["dg"][:, part])
+        assert np.all(tol < 0.05 * D.rms(ref["dg"][:, part]))
+        assert np.all(off <= tol), (i, off / tol)
