@@ -456,6 +456,23 @@ __global__ void __launch_bounds__(kThreads, MINB)
       }
       continue;
     }
+    if constexpr (!STATE_ONLY) {
+      // between tokens `edge` - 1 and `edge`: what the decay's gradient needs
+      const int64_t edge = job.reverse ? rows.first + 1 : rows.first;
+      if (job.anchor && edge % kLaAnchor == 0 && edge > 0 && edge < len) {
+        const int64_t at = edge / kLaAnchor;
+        float *dst =
+            job.anchor +
+            ((bh * p.anchors + (job.reverse ? p.anchors - at : at)) *
+                 job.tiles +
+             tile) *
+                SF;
+        Map::each([&](int n, int hr, int row, int col) {
+          *reinterpret_cast<float2 *>(dst + row * kLaTile + col) =
+              make_float2(S[n][2 * hr], S[n][2 * hr + 1]);
+        });
+      }
+    }
 
     {
       RawTile<T, QD> rk, rq;
@@ -861,12 +878,12 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-__device__ __forceinline__ float block_sum(float v, float *red) {
+__device__ __forceinline__ double block_sum(double v, double *red) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
   __syncthreads();
-  float s = 0.0f;
+  double s = 0.0;
   for (int w = 0; w < int(blockDim.x) / 32; ++w) s += red[w];
   __syncthreads();
   return s;
@@ -874,18 +891,23 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
 
 // The log decay's gradient. With G the gradient of the state,
 //   dg_t = <a_t S_{t-1}, G_t> = dg_{t+1} + q_t . dq_t - k_t . dk_t,
-// summed backwards inside each segment from its end, where the product of the
-// state and its gradient is formed from the two passes' segment states: the
-// differences are then never summed over more than one segment. A step that
+// summed backwards inside each group of steps from its end, where the product
+// of the state and its gradient is formed from the states the two passes left
+// there: what the differences are off by then adds up over one group only,
+// and the products' own errors over groups that know nothing of each other.
+// Where a float32 result comes of them, groups are kLaAnchor = 128 steps and
+// the sums 64-bit: of 2048 steps and in float32, the sum of a head's gradients
+// over 2 x 16384 steps was 2.7e-5 off (the plain form: 9e-7). Alone beside
+// bfloat16, segments of 2048 steps are as good as the output. A step that
 // starts the state anew has no gradient, and the sum starts from 0 there: the
 // differences behind it cancel in exact arithmetic only, and what rounding
 // leaves of them is not the business of the steps in front. One block per
-// (sequence, head, segment).
+// (sequence, head, group).
 template <typename T>
 __global__ void __launch_bounds__(256)
     linattn_gate_kernel(const __grid_constant__ LaGateParams p) {
-  __shared__ float red[8];
-  __shared__ float warp_tot[8];
+  __shared__ double red[8];
+  __shared__ double warp_tot[8];
   __shared__ bool warp_anew[8];
   const int64_t x = blockIdx.x;
   const int seg = int(x % p.nseg);
@@ -904,15 +926,15 @@ __global__ void __launch_bounds__(256)
   auto log2_of = [&](float g) {
     return (double(g) + head) * 1.4426950408889634;
   };
-  // the product of the state behind the segment and its gradient
+  // the product of the state behind the group and its gradient
   const float *S = nullptr, *G = nullptr;
   int64_t n = 0;
-  float end = 0.0f;
+  double end = 0.0;
   if (t1 < len) {
     S = p.fwd_state + (bh * p.nseg + seg + 1) * p.state_floats;
     G = p.rev_state + (bh * p.nseg + p.nseg - 1 - seg) * p.state_floats;
     n = p.state_floats;
-  } else if (p.dh_last) {
+  } else if (p.dh_last && t0 < len) {
     S = p.last_state + bh * p.last_floats;
     G = p.dh_last + bh * p.last_floats;
     n = p.last_floats;
@@ -921,31 +943,32 @@ __global__ void __launch_bounds__(256)
     float s = 0.0f;
 #pragma unroll 16
     for (int64_t i = threadIdx.x; i < n; i += 256) s = fmaf(S[i], G[i], s);
-    end = block_sum(s, red);
-    if (t1 < len) {  // the decay of the next segment's first token
+    end = block_sum(double(s), red);
+    if (t1 < len) {  // the decay of the next group's first token
       const float a = ex2_d(log2_of(
           p.log_decay ? to_f(static_cast<const T *>(
                             p.log_decay)[(b * L + t1) * p.heads + h])
                       : 0.0f));
-      end = a == 0.0f ? 0.0f : end * a;
+      end = a == 0.0f ? 0.0 : end * double(a);
     }
   }
   // backwards, a whole segment at a time where it is one of 2048: thread i has
   // the i-th kRun tokens from the end, all on their way at once (8 x 24 heads
   // of 2048 tokens: 18 us with a token a thread in eight rounds, 13.5 so)
   constexpr int kRun = 8;
-  float carry = end, part = 0.0f;
+  double carry = end, part = 0.0;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   for (int64_t hi = t1; hi > t0; hi -= 256 * kRun) {
     const int64_t last = hi - 1 - int64_t(threadIdx.x) * kRun;
-    float v[kRun], u[kRun];
+    double v[kRun];
+    float u[kRun], w[kRun];
     T g[kRun];
     auto in = [&](int j) { return last - j >= t0 && last - j < len; };
     const int64_t at = (b * p.heads + h) * L + last;
     const int64_t step = p.batch * p.heads * L;
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-      v[j] = in(j) ? p.rows_q[at - j] : 0.0f;
+      w[j] = in(j) ? p.rows_q[at - j] : 0.0f;
       u[j] = in(j) ? p.rows_k[at - j] : 0.0f;
     }
 #pragma unroll
@@ -955,12 +978,12 @@ __global__ void __launch_bounds__(256)
                        p.log_decay)[(b * L + last - j) * p.heads + h]
                  : T(0.0f);
 #pragma unroll
-    for (int j = 0; j < kRun; ++j) v[j] -= u[j];
+    for (int j = 0; j < kRun; ++j) v[j] = double(w[j]) - double(u[j]);
     for (int k = 1; k < p.parts; ++k) {
       const float *q = p.rows_q + k * step, *r = p.rows_k + k * step;
 #pragma unroll
       for (int j = 0; j < kRun; ++j)
-        if (in(j)) v[j] += q[at - j] - r[at - j];
+        if (in(j)) v[j] += double(q[at - j]) - double(r[at - j]);
     }
     // sums since the last restart behind each token; `anew`: there is one in
     // this thread's tokens so far (bits), its warp's, the block's
@@ -969,13 +992,13 @@ __global__ void __launch_bounds__(256)
     for (int j = 0; j < kRun; ++j) {
       const bool starts = in(j) && log2_of(to_f(g[j])) < -126.0;
       anew |= uint32_t(starts) << j;
-      v[j] = starts ? 0.0f : j ? v[j] + v[j - 1] : v[j];
+      v[j] = starts ? 0.0 : j ? v[j] + v[j - 1] : v[j];
     }
-    float sum = v[kRun - 1];
+    double sum = v[kRun - 1];
     int any = anew != 0u;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const float o = __shfl_up_sync(0xffffffffu, sum, d);
+      const double o = __shfl_up_sync(0xffffffffu, sum, d);
       const int oa = __shfl_up_sync(0xffffffffu, any, d);
       if (lane >= d && !any) {
         sum += o;
@@ -987,17 +1010,17 @@ __global__ void __launch_bounds__(256)
       warp_anew[warp] = any;
     }
     // what lies behind this thread's tokens in its warp
-    float before = __shfl_up_sync(0xffffffffu, sum, 1);
+    double before = __shfl_up_sync(0xffffffffu, sum, 1);
     int cut = __shfl_up_sync(0xffffffffu, any, 1);
     if (lane == 0) {
-      before = 0.0f;
+      before = 0.0;
       cut = 0;
     }
     __syncthreads();
-    float behind = carry;
-    for (int w = 0; w < 8; ++w) {
-      if (w == warp && !cut) before += behind;
-      behind = warp_anew[w] ? warp_tot[w] : behind + warp_tot[w];
+    double behind = carry;
+    for (int i = 0; i < 8; ++i) {
+      if (i == warp && !cut) before += behind;
+      behind = warp_anew[i] ? warp_tot[i] : behind + warp_tot[i];
     }
     carry = behind;
     __syncthreads();
@@ -1008,9 +1031,10 @@ __global__ void __launch_bounds__(256)
         // (a step that starts the state anew does not depend on its decay)
         const bool live = t < len && !(anew >> j & 1u);
         const bool whole = (anew & ((2u << j) - 1u)) == 0u;
-        const float out = live ? (whole ? before + v[j] : v[j]) : 0.0f;
+        const double out = live ? (whole ? before + v[j] : v[j]) : 0.0;
         if (p.dlog_decay)
-          static_cast<T *>(p.dlog_decay)[(b * L + t) * p.heads + h] = T(out);
+          static_cast<T *>(p.dlog_decay)[(b * L + t) * p.heads + h] =
+              T(float(out));
         part += out;
       }
     }
@@ -1023,13 +1047,13 @@ __global__ void __launch_bounds__(256)
 
 // out[h] = sum over n rows of part[n][heads], in a fixed order.
 __global__ void __launch_bounds__(128)
-    linattn_head_sum_kernel(const float *part, int64_t n, int heads,
+    linattn_head_sum_kernel(const double *part, int64_t n, int heads,
                             float *out) {
   __shared__ double red[4];
   const int h = blockIdx.x;
   double s = 0.0;
   for (int64_t i = threadIdx.x; i < n; i += 128)
-    s += double(part[i * heads + h]);
+    s += part[i * heads + h];
   for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
   if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = s;
   __syncthreads();

@@ -9,6 +9,9 @@ namespace ssm {
 constexpr int kLaChunk = 64;   // steps per chunk of the chunked form
 constexpr int kLaTile = 64;    // value columns per block
 constexpr int kLaMaxKey = 128; // widest key (and, backward, value)
+// Steps from one state that the decay's gradient is anchored to to the next
+// (kernel_linattn.cuh), a multiple of the chunk.
+constexpr int kLaAnchor = 128;
 
 // One pass of linear attention with decay over every sequence and head:
 //   y_i = sp * sum_{j <= i} decay(j, i) (q_i . k_j) v_j + si * (...) of the
@@ -35,6 +38,9 @@ struct LaJob {
                                          // of 32 columns each
   float *seg_state;                      // [bhs, nseg, tiles, QD, 64]
   float *seg_decay;                      // [bhs, nseg]
+  float *anchor;                         // [b, heads, anchors, tiles, QD, 64]
+                                         // or nullptr: the state in front of
+                                         // every kLaAnchor-th token
 };
 
 struct LaParams {
@@ -46,21 +52,23 @@ struct LaParams {
   int heads;
   int nseg;                     // segments per sequence
   int64_t seg_len;              // steps per segment, a multiple of the chunk
+  int anchors;                  // groups of kLaAnchor tokens in a sequence
   int bh0, bhs;                 // the sequences' heads of this launch, counted
                                 // through all: bhs of them from bh0 on
 };
 
-// The log decay's gradient from the row dots and the states at the segments'
-// ends.
+// The log decay's gradient from the row dots and the states at the ends of
+// groups of steps (nseg of seg_len steps: kLaAnchor of them, or a segment).
 struct LaGateParams {
   const float *rows_q, *rows_k;  // row dots of dq with q, of dk with k
   int parts;                           // of 32 columns each
-  const float *fwd_state, *rev_state;  // seg_state of the dq and dk passes
-  int64_t state_floats;                // floats of one (segment, all tiles)
+  const float *fwd_state, *rev_state;  // anchor (seg_state) of the dq and dk
+                                       // passes
+  int64_t state_floats;                // floats of one state, all tiles
   const float *last_state, *dh_last;   // [b, H, dk, dv], dh_last or nullptr
   int64_t last_floats;                 // dk dv
   void *dlog_decay;                    // [b, L, H] activation type or nullptr
-  float *part;                         // [b, nseg, H] sums or nullptr
+  double *part;                        // [b, nseg, H] sums or nullptr
   const void *log_decay;
   const float *head_log_decay;
   const int *lengths;

@@ -27,8 +27,10 @@ constexpr int64_t kMaxSteps = int64_t(1) << 36;
 // The tensor-memory kernel counts tokens in 32 bits, up to two chunks past the
 // end.
 constexpr int64_t kMaxTcSteps = int64_t(1) << 30;
-// The decay's gradient sums differences inside a segment: a bounded segment
-// bounds how many of them are added up.
+// The decay's gradient sums differences inside a group of steps. The
+// tensor-memory kernel's passes, which run where that gradient is bfloat16
+// (rounded by 2^-9), leave states at the ends of segments only, and the segment
+// is the group; the other kernel's leave one every kLaAnchor steps.
 constexpr int64_t kGateSegment = 2048;
 
 // Shared memory that lets one block of the tensor-memory kernel (which takes
@@ -79,7 +81,10 @@ struct Plan {
   // byte offsets into the workspace; jobs: y or dq, dk, dv
   size_t state[3] = {0, 0, 0}, decay[3] = {0, 0, 0};
   size_t part_dq = 0, part_dk = 0, rows_q = 0, rows_k = 0, part_head = 0,
-         last = 0;
+         last = 0, anchor[2] = {0, 0};
+  // groups of steps that the decay's gradient is summed in (backward)
+  int groups = 0;
+  int64_t group_len = 0;
   size_t bytes = 0;
 };
 
@@ -145,7 +150,8 @@ Plan plan_bwd(const ssm_linattn_dims &d, Path path, bool gate, int sms) {
                 tv = ceil_div(d.dv, ssm::kLaTile);
   const size_t bh = size_t(d.batch) * d.heads;
   cut(&pl, d.batch * d.heads * (path == Path::kTc ? 3 : 2 * tk + tv),
-      d.seqlen, sms, path, gate ? kGateSegment : int64_t(1) << 40);
+      d.seqlen, sms, path,
+      gate && path == Path::kTc ? kGateSegment : int64_t(1) << 40);
   if (pl.nseg > 1)
     for (int j = 0; j < 3; ++j) {
       pl.state[j] = take(&pl.bytes, bh * pl.nseg * (j < 2 ? tk : tv) *
@@ -160,7 +166,17 @@ Plan plan_bwd(const ssm_linattn_dims &d, Path path, bool gate, int sms) {
   if (gate) {
     pl.rows_q = take(&pl.bytes, bh * d.seqlen * 2 * tk);
     pl.rows_k = take(&pl.bytes, bh * d.seqlen * 2 * tk);
-    pl.part_head = take(&pl.bytes, bh * pl.nseg);
+    pl.groups = pl.nseg;
+    pl.group_len = pl.seg_len;
+    if (path == Path::kAny) {
+      pl.groups = int(ceil_div(d.seqlen, ssm::kLaAnchor));
+      pl.group_len = ssm::kLaAnchor;
+      if (pl.groups > 1)
+        for (size_t &a : pl.anchor)
+          a = take(&pl.bytes, bh * pl.groups * tk * key_pad(d.dv) *
+                                  ssm::kLaTile);
+    }
+    pl.part_head = take(&pl.bytes, bh * pl.groups * 2);  // 64-bit
     pl.last = take(&pl.bytes, bh * d.dk * d.dv);
   }
   return pl;
@@ -360,6 +376,7 @@ LaParams common(const ssm_linattn_dims &d, const Plan &pl,
   p.heads = int(d.heads);
   p.nseg = pl.nseg;
   p.seg_len = pl.seg_len;
+  p.anchors = pl.groups;
   p.bhs = int(d.batch * d.heads);
   return p;
 }
@@ -585,6 +602,8 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
   if (pl.bytes > workspace_bytes || (pl.bytes && !workspace))
     return SSM_ERR_INVALID;
   if (workspace && !aligned(workspace, 16)) return SSM_ERR_ALIGN;
+  if (gate && dims.batch * dims.heads > 0x7fffffff / pl.groups)
+    return SSM_ERR_UNSUPPORTED;
   unsigned char *ws = static_cast<unsigned char *>(workspace);
   auto at = [&](size_t off) { return reinterpret_cast<float *>(ws + off); };
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -633,6 +652,10 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
     jq.rows = at(pl.rows_q);
     jk.rows = at(pl.rows_k);
     if (dh_last) jq.last = at(pl.last);  // [dk, dv] through the strides
+    if (path == Path::kAny && pl.groups > 1) {
+      jq.anchor = at(pl.anchor[0]);
+      jk.anchor = at(pl.anchor[1]);
+    }
   }
 
   LaParams p = common(dims, pl, log_decay, head_log_decay, lengths);
@@ -668,30 +691,31 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
     g.rows_k = at(pl.rows_k);
     // the other kernel's passes leave row dots for each 32 columns
     g.parts = path == Path::kTc ? 1 : 2 * jq.tiles;
-    if (pl.nseg > 1) {
-      g.fwd_state = at(pl.state[0]);
-      g.rev_state = at(pl.state[1]);
+    if (pl.groups > 1) {
+      g.fwd_state = path == Path::kAny ? jq.anchor : jq.seg_state;
+      g.rev_state = path == Path::kAny ? jk.anchor : jk.seg_state;
     }
     g.state_floats = int64_t(jq.tiles) * key_pad(V) * ssm::kLaTile;
     g.last_state = at(pl.last);
     g.dh_last = dh_last;
     g.last_floats = int64_t(K) * V;
     g.dlog_decay = dlog_decay;
-    g.part = dhead_log_decay ? at(pl.part_head) : nullptr;
+    g.part = dhead_log_decay
+                 ? reinterpret_cast<double *>(ws + pl.part_head)
+                 : nullptr;
     g.log_decay = log_decay;
     g.head_log_decay = head_log_decay;
     g.lengths = lengths;
     g.batch = dims.batch; g.seqlen = dims.seqlen; g.heads = H;
-    g.nseg = pl.nseg; g.seg_len = pl.seg_len;
-    const int64_t grid = dims.batch * H * pl.nseg;
-    if (grid > 0x7fffffff) return SSM_ERR_UNSUPPORTED;
+    g.nseg = pl.groups; g.seg_len = pl.group_len;
+    const int64_t grid = dims.batch * H * pl.groups;
     if (dtype == SSM_F32)
       ssm::la::linattn_gate_kernel<float><<<unsigned(grid), 256, 0, s>>>(g);
     else
       ssm::la::linattn_gate_kernel<bf16><<<unsigned(grid), 256, 0, s>>>(g);
     if (dhead_log_decay)
       ssm::la::linattn_head_sum_kernel<<<H, 128, 0, s>>>(
-          g.part, dims.batch * pl.nseg, H, dhead_log_decay);
+          g.part, dims.batch * pl.groups, H, dhead_log_decay);
     if (cudaGetLastError() != cudaSuccess) return SSM_ERR_CUDA;
   }
   return SSM_OK;

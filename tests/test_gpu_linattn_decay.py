@@ -68,3 +68,71 @@ def test_packed_documents_keep_their_own_scale(attn, path):
             + (4 * 2.0 ** -22 + M.U[dtype]) * D.rms(ref["dg"][:, part])
         assert np.all(tol < 0.05 * D.rms(ref["dg"][:, part]))
         assert np.all(off <= tol), (i, off / tol)
+
+
+# steps from an anchor to the next: 128, or a segment (of 2048 at most) where
+# the gradient is bfloat16 and comes of the tensor-memory kernel
+LONG = {"f32": 128, "bf16_head": 128, "bf16_token": 2048}
+
+
+@pytest.mark.parametrize("path", sorted(LONG))
+@pytest.mark.parametrize("b,L,state", [(1, 8192, False), (2, 2049, True),
+                                       (1, 4223, True), (3, 300, True)])
+@pytest.mark.parametrize("rate", [0.1, 0.003])
+def test_long_sums(attn, path, b, L, state, rate):
+    dtype, gate, planes = PATHS[path]
+    c = Case(dtype, b, L, 2, 2, 32, 32, gate=gate, state=state, rate=rate)
+    ref = reference(c)
+    each, total = D.tolerances(c, ref, LONG[path], D.DELTA[planes], dtype)
+    size = D.sizes(c, ref)[1]
+    assert np.all(each <= 0.02 * size)
+    g = c.run_back(attn)
+    off = D.rms(host(g["dlog_decay"]) - ref["dg"])
+    print("each", off / each)
+    assert np.all(off <= each), off / each
+    if g["dhead_log_decay"] is not None:
+        off = np.abs(host(g["dhead_log_decay"]) - ref["dhead"])
+        print("total", off / total)
+        assert np.all(off <= total), off / total
+
+
+@pytest.mark.parametrize("path", sorted(LONG))
+def test_long_sums_where_heads_fill_the_gpu(attn, path):
+    """Sequences that are not cut for want of heads are not summed in longer
+    pieces for it."""
+    dtype, gate, planes = PATHS[path]
+    c = Case(dtype, 1, 6144, 64, 64, 8, 8, gate=gate, state=False, rate=0.003)
+    ref = reference(c)
+    each, total = D.tolerances(c, ref, LONG[path], D.DELTA[planes], dtype)
+    assert np.all(each <= 0.05 * D.sizes(c, ref)[1])
+    g = c.run_back(attn)
+    off = D.rms(host(g["dlog_decay"]) - ref["dg"]) / each
+    print("each", off.max())
+    assert np.all(off <= 1), off
+    if g["dhead_log_decay"] is not None:
+        off = np.abs(host(g["dhead_log_decay"]) - ref["dhead"]) / total
+        print("total", off.max())
+        assert np.all(off <= 1), off
+
+
+@pytest.mark.parametrize("path", sorted(LONG))
+def test_long_sums_of_padded_sequences(attn, path):
+    """A padded batch gives, sequence by sequence, what the sequences alone
+    are bound to."""
+    dtype, gate, planes = PATHS[path]
+    lengths = [2500, 0, 128, 1025]
+    c = Case(dtype, 4, 2500, 2, 2, 32, 32, gate=gate, lengths=lengths)
+    ref = reference(c)
+    got = host(c.run_back(attn)["dlog_decay"])
+    m = ((c.q * ref["dq"]) ** 2).sum(-1) + ((c.k * ref["dk"]) ** 2).sum(-1)
+    for i, n in enumerate(lengths):
+        assert not got[i, n:].any()
+        if n == 0:
+            continue
+        dg = np.sqrt((ref["dg"][i, :n] ** 2).mean(0))
+        tol = 4 * (D.DELTA[planes] * np.sqrt(m[i, :n].mean(0))
+                   * np.sqrt(min(n, LONG[path])) + 2.0 ** -22 * dg) \
+            + M.U[dtype] * dg
+        assert np.all(tol <= 0.02 * dg)
+        off = np.sqrt(((got[i, :n] - ref["dg"][i, :n]) ** 2).mean(0))
+        assert np.all(off <= tol), (i, off / tol)
