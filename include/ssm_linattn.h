@@ -21,8 +21,8 @@
  *     v_stride are the elements from one token to the next (0: dense), and a
  *     sequence is seqlen of them. All else is dense.
  *   - Either decay may be NULL (0). A log decay of -infinity, or one below
- *     -87 (where its exponential leaves float32), starts the state anew at
- *     its token, whatever the state held. Others are finite numbers; positive
+ *     -87 (where its exponential is about to leave float32's normal numbers),
+ *     starts the state anew at its token, whatever the state held. Others are finite numbers; positive
  *     ones are taken as they are.
  *   - lengths: NULL means every sequence has seqlen tokens. Else sequence b has
  *     lengths[b] of them (values outside 0..seqlen count as the nearer bound):

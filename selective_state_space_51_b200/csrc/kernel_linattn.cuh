@@ -211,9 +211,13 @@ __device__ __forceinline__ void prefetch_tile(const T *src, int64_t stride,
   }
 }
 
-// The chunk's decays, in units of log2. A log decay below -87 makes e^g
-// exactly 0 in float32: such a step starts the state anew, the sums restart
-// there (so that they stay finite and small) and nothing before it is read.
+// A step whose log decay is below this starts the state anew (e^g is about to
+// leave float32's normal numbers, which end at e^-87.3).
+constexpr double kRestart = -87.0;
+
+// The chunk's decays, in units of log2. At a step that starts the state anew
+// the sums restart (so that they stay finite and small), and nothing before it
+// is read.
 // The sums are formed in 64 bits and kept as a pair of floats: a difference of
 // two of them is then exact to float32 however much the chunk decays.
 struct alignas(16) Gates {
@@ -232,6 +236,11 @@ __device__ __forceinline__ float ex2_d(double x) {
   return ex2(hi) * fmaf(float(x - double(hi)), kLn2, 1.0f);
 }
 
+// The decay of one step, from its log decay.
+__device__ __forceinline__ float decay_of(double g) {
+  return g < kRestart ? 0.0f : ex2_d(g * 1.4426950408889634);
+}
+
 template <typename T>
 __device__ __forceinline__ void load_gates(Gates &g, const LaParams &p,
                                            const Rows &rows, int64_t b,
@@ -247,13 +256,13 @@ __device__ __forceinline__ void load_gates(Gates &g, const LaParams &p,
     const int r = 2 * lane + j;
     const int64_t t = rows.token(r) + (reverse ? 1 : 0);
     double x = 0.0;
-    if (t < rows.len) x = gate_at<T>(p, b, t, h) * 1.4426950408889634;
-    if (x < -126.0) {
+    if (t < rows.len) x = gate_at<T>(p, b, t, h);
+    if (x < kRestart) {
       sum = 0.0;
       last = r;
       any = true;
     } else {
-      sum += x;
+      sum += x * 1.4426950408889634;
     }
     c[j] = sum;
     from[j] = any ? last : -1;
@@ -823,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
     // running backwards, the first token's own decay is still to come
     float f = 1.0f;
     if (job.reverse && len > 0)
-      f = ex2_d(gate_at<T>(p, b, 0, h) * 1.4426950408889634);
+      f = decay_of(gate_at<T>(p, b, 0, h));
     float *dst = job.last + bh * job.qd * job.vd;
     Map::each([&](int n, int hr, int row, int col) {
 #pragma unroll
@@ -923,9 +932,7 @@ __global__ void __launch_bounds__(256)
   const int64_t t0 = int64_t(seg) * p.seg_len;
   const int64_t t1 = t0 + p.seg_len;
   const double head = p.head_log_decay ? double(p.head_log_decay[h]) : 0.0;
-  auto log2_of = [&](float g) {
-    return (double(g) + head) * 1.4426950408889634;
-  };
+  auto log_of = [&](float g) { return double(g) + head; };
   // the product of the state behind the group and its gradient
   const float *S = nullptr, *G = nullptr;
   int64_t n = 0;
@@ -945,7 +952,7 @@ __global__ void __launch_bounds__(256)
     for (int64_t i = threadIdx.x; i < n; i += 256) s = fmaf(S[i], G[i], s);
     end = block_sum(double(s), red);
     if (t1 < len) {  // the decay of the next group's first token
-      const float a = ex2_d(log2_of(
+      const float a = decay_of(log_of(
           p.log_decay ? to_f(static_cast<const T *>(
                             p.log_decay)[(b * L + t1) * p.heads + h])
                       : 0.0f));
@@ -990,7 +997,7 @@ __global__ void __launch_bounds__(256)
     uint32_t anew = 0u;
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-      const bool starts = in(j) && log2_of(to_f(g[j])) < -126.0;
+      const bool starts = in(j) && log_of(to_f(g[j])) < kRestart;
       anew |= uint32_t(starts) << j;
       v[j] = starts ? 0.0 : j ? v[j] + v[j - 1] : v[j];
     }
@@ -1127,7 +1134,7 @@ __global__ void __launch_bounds__(256)
   if (p.log_decay)
     gd = double(to_f(static_cast<const T *>(p.log_decay)[bh]));
   if (p.head_log_decay) gd += double(p.head_log_decay[h]);
-  const float a = ex2_d(gd * 1.4426950408889634);
+  const float a = decay_of(gd);
   float v[W], y[W];
 #pragma unroll
   for (int j = 0; j < W; ++j) {

@@ -135,7 +135,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     linattn_tc_kernel(const __grid_constant__ Params pp) {
   using L_ = Lay<QD, TV, PS, STATE_ONLY>;
   using la::bf16;
-  using la::ex2_d;
   using la::pack2;
   extern __shared__ __align__(1024) unsigned char smem[];
   Gates &gt = *reinterpret_cast<Gates *>(smem + L_::GATES);
@@ -466,11 +465,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 4; ++j) {
           const double g =
               it >= 0 && token(it, j) < len
-                  ? (double(__uint_as_float(uint32_t(raw[j]) << 16)) + head) *
-                        1.4426950408889634
+                  ? double(__uint_as_float(uint32_t(raw[j]) << 16)) + head
                   : 0.0;
-          sum += g;
-          if (g < -126.0) {
+          sum += g * 1.4426950408889634;
+          if (g < la::kRestart) {
             sum = 0.0;
             lastr = 4 * lane + j;
           }
@@ -771,8 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       stride = job.state_rs;
       // running backwards, the first token's own decay is still to come
       if (rev && len > 0) {
-        const float f =
-            ex2_d(la::gate_at<bf16>(p, b, 0, h) * 1.4426950408889634);
+        const float f = la::decay_of(la::gate_at<bf16>(p, b, 0, h));
 #pragma unroll
         for (int i = 0; i < QD; ++i) S[i] = f == 0.0f ? 0.0f : S[i] * f;
       }
