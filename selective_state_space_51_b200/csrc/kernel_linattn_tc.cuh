@@ -28,6 +28,8 @@
 //
 // A wait by parity has to come within one phase of its barrier: every wait
 // here is for a phase that cannot be followed by the next before it returns.
+// Whichever role gives a wait up says so itself (`dead`): the last chunk's are
+// waited for by nobody else.
 //
 // The decay e^{c_i - c_j}: outside the 32 x 32 blocks on the diagonal it is
 // e^{c_i - c_r} e^{c_r - c_j}, r the last step of j's block: both factors are
@@ -431,9 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!alive) gt.dead = 1;
       // every product is done before the block goes
       tc::commit(e, bar(kFin));
+      int left = 1 << 16;
 #pragma unroll 1
-      for (int i = 0; i < 1 << 16; ++i)
-        if (tc::bar_try(bar(kFin), 0)) break;
+      while (left > 0 && !tc::bar_try(bar(kFin), 0)) --left;
+      if (left == 0) gt.dead = 1;
       __syncwarp();
     } else {
       // ---- decays: every second chunk each, four steps a lane in the order
@@ -543,6 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) tc::bar_arrive(bar(kGates));
         }
       }
+      if (!alive) gt.dead = 1;
     }
   } else if (warp < 4) {
     // ---- scores: P -> P'
@@ -550,8 +554,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the step of this row in time, and its warp's block of 32
     const int step = rev ? kChunk - 1 - r : r;
     const int tb = rev ? 3 - warp : warp;
+    int it = 0;
 #pragma unroll 1
-    for (int it = 0; it < n_live; ++it) {
+    for (; it < n_live; ++it) {
       if (!chunk_in(it) || (it == ragged && !wait(kClean, 0)) || !weigh(it, 0))
         break;
       tc::bar_arrive(bar(kWeightsFree0 + (it & 1)));
@@ -644,6 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::before_sync();
       tc::bar_arrive(bar(kScored));
     }
+    if (it < n_live) gt.dead = 1;
   } else if (warp < 8) {
     // ---- the weighted values and the state; lane: a value column
     tc::more_registers<208>();
@@ -804,8 +810,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // In turn: O1 of chunk it is scaled, slot 1 of chunk it + 1 weighed
       // (while the output's products run), chunk it put out.
+      int it = -1;
 #pragma unroll 1
-      for (int it = -1; it < n_live; ++it) {
+      for (; it < n_live; ++it) {
         const int st = it & 1;
         if (!STATE_ONLY && it >= 0) {
           // O1, scaled in its place: O2 is added to it there
@@ -909,6 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (job.rows && t < L) job.rows[(b * p.heads + h) * L + t] = dot;
       }
+      if (it < n_live) gt.dead = 1;
     }
   }
   tc::before_sync();
