@@ -43,17 +43,45 @@ def launch(torch, device, stream, call, *args):
     """call(raw stream, *args) with `device` current and torch's allocations
     made on that stream (so that a workspace or a result is never handed to,
     or taken from, work that another stream still has to do). stream: None
-    for torch's current stream of the device, a torch stream or a raw one."""
+    for torch's current stream of the device, a torch stream or a raw one.
+
+    On another stream than the current one the call comes behind what the
+    current stream has been given so far, and the memory of the tensors among
+    `args` is not given to anyone else before it is done. A raw stream may go
+    before they do, so there the caller keeps them. A call that is captured on
+    `stream` while the current stream is not being captured waits for nothing:
+    a graph cannot depend on work outside."""
     index = device.index
     if stream is None:
         if torch.cuda.current_device() == index:
             return call(torch._C._cuda_getCurrentRawStream(index), *args)
         with torch.cuda.device(device):
             return call(torch._C._cuda_getCurrentRawStream(index), *args)
-    if isinstance(stream, int):
+    raw = isinstance(stream, int)
+    if raw:
         stream = torch.cuda.ExternalStream(stream, device=device)
     if stream.device != device:
         raise ValueError("stream belongs to %s, not %s" % (stream.device,
                                                            device))
+    here = torch.cuda.current_stream(device)
+    if stream.cuda_stream == here.cuda_stream:
+        with torch.cuda.device(device):
+            return call(stream.cuda_stream, *args)
     with torch.cuda.stream(stream):   # also makes its device current
-        return call(stream.cuda_stream, *args)
+        if not torch.cuda.is_current_stream_capturing() or \
+                _captured(torch, here):
+            stream.wait_stream(here)
+        result = call(stream.cuda_stream, *args)
+    if not raw:
+        for t in args:
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
+    return result
+
+
+def _captured(torch, stream):
+    """(The default stream cannot be, and asking may be an error.)"""
+    if stream.cuda_stream == 0:
+        return False
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()

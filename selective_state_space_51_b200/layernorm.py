@@ -44,7 +44,8 @@ class LayerNorm:
 
     x, residual: contiguous [..., D], float32 or bfloat16; weight, bias: [D]
     float32 or None. The object keeps no device memory: calls may run at once
-    on several streams and threads, and be captured into CUDA graphs.
+    on several streams and threads, and be captured into CUDA graphs. stream:
+    as for LinearAttention.
     """
 
     def __init__(self, device: int = 0):

@@ -78,6 +78,12 @@ class LinearAttention:
     be slices of wider rows; everything else is contiguous. scale defaults to
     dk ** -0.5. The object keeps no device memory: calls may run at once on
     several streams and threads, and be captured into CUDA graphs.
+
+    stream: None for torch's current stream, a torch stream or a raw one. On
+    another stream than the current one a call comes behind what the current
+    stream has been given so far, and its tensors' memory is kept until it is
+    done (with a raw stream the caller keeps it); its results belong to
+    `stream`, and work on other streams that reads them waits for it.
     """
 
     def __init__(self, device: int = 0):
