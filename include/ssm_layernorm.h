@@ -66,8 +66,8 @@ SSM_API int ssm_layernorm_workspace(int device, int64_t rows, int64_t dim,
  *   dweight, dbias : NULL means not wanted.
  *   workspace  : at least ssm_layernorm_workspace bytes, used until the call
  *                is done on `stream`; NULL when neither sum is wanted.
- * dx may be dy, x or dsum itself. Nothing else that is written may overlap
- * anything (SSM_ERR_INVALID).
+ * dx may be dy, x or dsum itself. Nothing else that is written, the workspace
+ * included, may overlap anything (SSM_ERR_INVALID).
  */
 SSM_API int ssm_layernorm_bwd(int device, const void *dy, const void *x,
                               const float *mean, const float *rstd,

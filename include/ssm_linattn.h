@@ -88,7 +88,8 @@ SSM_API int ssm_linattn_workspace(int device, ssm_linattn_dims dims, int dtype,
  *   h_last : NULL means the last state is not written. It may be h0.
  *   workspace : at least ssm_linattn_workspace bytes, 16-byte aligned, used
  *            until the call is done on `stream`; NULL where that is 0.
- * y and h_last must not overlap each other or (else) an input.
+ * y and h_last must not overlap each other or (else) an input, nor the
+ * workspace any of these.
  */
 SSM_API int ssm_linattn_fwd(int device, const void *q, const void *k,
                             const void *v, const void *log_decay,
@@ -121,7 +122,7 @@ SSM_API int ssm_linattn_step(int device, const void *q, const void *k,
  *   dh0    : [batch, heads, dk, dv] float32, or NULL.
  *   workspace : as above, for backward != 0.
  * The log decays' gradients at a token that starts the state anew are 0.
- * No output may overlap another or an input.
+ * No output, and not the workspace, may overlap another or an input.
  */
 SSM_API int ssm_linattn_bwd(int device, const void *q, const void *k,
                             const void *v, const void *log_decay,

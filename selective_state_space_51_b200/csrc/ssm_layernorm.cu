@@ -285,10 +285,14 @@ int ssm_layernorm_bwd(int device, const void *dy, const void *x,
   p.wpr = s.wpr;
   p.parts = parts_of(s, rows, sms);
   if (dweight || dbias) {
-    if (!workspace ||
-        workspace_bytes < size_t(p.parts) * 2 * dim * sizeof(float))
-      return SSM_ERR_INVALID;
+    const size_t need = size_t(p.parts) * 2 * dim * sizeof(float);
+    if (!workspace || workspace_bytes < need) return SSM_ERR_INVALID;
     if (!aligned(workspace, 4)) return SSM_ERR_ALIGN;
+    if (ssm::clash({{workspace, need}},
+                   {{dx, all}, {dweight, row}, {dbias, row}, {dy, all},
+                    {x, all}, {dsum, all}, {mean, stats}, {rstd, stats},
+                    {weight, row}}))
+      return SSM_ERR_INVALID;
     p.part = static_cast<float *>(workspace);
   }
   return run(p, wide, true, dtype, s, sms,

@@ -439,15 +439,14 @@ int ssm_linattn_fwd(int device, const void *q, const void *k, const void *v,
   const ssm::Span out_y = rows_span(y, dims, H, H, esz),
                   in_h = state_span(h0 == h_last ? nullptr : h0, dims),
                   out_h = state_span(h_last, dims);
-  if (ssm::clash({out_y, out_h},
-                 {rows_span(q, dims, dims.q_stride, G, esz),
-                  rows_span(k, dims, dims.k_stride, G, esz),
-                  rows_span(v, dims, dims.v_stride, H, esz),
-                  rows_span(log_decay, dims, dims.heads, dims.heads, esz),
-                  {head_log_decay, size_t(dims.heads) * sizeof(float)},
-                  {lengths, size_t(dims.batch) * sizeof(int32_t)},
-                  in_h}))
-    return SSM_ERR_INVALID;
+  const auto reads = {
+      rows_span(q, dims, dims.q_stride, G, esz),
+      rows_span(k, dims, dims.k_stride, G, esz),
+      rows_span(v, dims, dims.v_stride, H, esz),
+      rows_span(log_decay, dims, dims.heads, dims.heads, esz),
+      ssm::Span{head_log_decay, size_t(dims.heads) * sizeof(float)},
+      ssm::Span{lengths, size_t(dims.batch) * sizeof(int32_t)}, in_h};
+  if (ssm::clash({out_y, out_h}, reads)) return SSM_ERR_INVALID;
   int sms = 0;
   rc = ssm::device_ready(device, &sms);
   if (rc != SSM_OK) return rc;
@@ -457,6 +456,8 @@ int ssm_linattn_fwd(int device, const void *q, const void *k, const void *v,
   if (pl.bytes > workspace_bytes || (pl.bytes && !workspace))
     return SSM_ERR_INVALID;
   if (workspace && !aligned(workspace, 16)) return SSM_ERR_ALIGN;
+  if (pl.bytes && ssm::clash({{workspace, pl.bytes}, out_y, out_h}, reads))
+    return SSM_ERR_INVALID;
   unsigned char *ws = static_cast<unsigned char *>(workspace);
 
   LaParams p = common(dims, pl, log_decay, head_log_decay, lengths);
@@ -571,20 +572,23 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
   const int64_t dy_stride = int64_t(H) * V;
   const size_t heads_bytes = size_t(H) * sizeof(float);
   const int64_t qk = int64_t(G) * K;
-  if (ssm::clash({rows_span(dq, dims, qk, qk, esz),
-                  rows_span(dk, dims, qk, qk, esz),
-                  rows_span(dv, dims, dy_stride, dy_stride, esz),
-                  rows_span(dlog_decay, dims, H, H, esz),
-                  {dhead_log_decay, heads_bytes}, state_span(dh0, dims)},
-                 {rows_span(q, dims, dims.q_stride, qk, esz),
-                  rows_span(k, dims, dims.k_stride, qk, esz),
-                  rows_span(v, dims, dims.v_stride, dy_stride, esz),
-                  rows_span(log_decay, dims, H, H, esz),
-                  {head_log_decay, heads_bytes},
-                  {lengths, size_t(dims.batch) * sizeof(int32_t)},
-                  state_span(h0, dims),
-                  rows_span(dy, dims, dy_stride, dy_stride, esz),
-                  state_span(dh_last, dims)}))
+  const ssm::Span writes[] = {
+      rows_span(dq, dims, qk, qk, esz), rows_span(dk, dims, qk, qk, esz),
+      rows_span(dv, dims, dy_stride, dy_stride, esz),
+      rows_span(dlog_decay, dims, H, H, esz),
+      ssm::Span{dhead_log_decay, heads_bytes}, state_span(dh0, dims)};
+  const auto reads = {
+      rows_span(q, dims, dims.q_stride, qk, esz),
+      rows_span(k, dims, dims.k_stride, qk, esz),
+      rows_span(v, dims, dims.v_stride, dy_stride, esz),
+      rows_span(log_decay, dims, H, H, esz),
+      ssm::Span{head_log_decay, heads_bytes},
+      ssm::Span{lengths, size_t(dims.batch) * sizeof(int32_t)},
+      state_span(h0, dims), rows_span(dy, dims, dy_stride, dy_stride, esz),
+      state_span(dh_last, dims)};
+  if (ssm::clash({writes[0], writes[1], writes[2], writes[3], writes[4],
+                  writes[5]},
+                 reads))
     return SSM_ERR_INVALID;
   int sms = 0;
   rc = ssm::device_ready(device, &sms);
@@ -602,6 +606,11 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
   if (pl.bytes > workspace_bytes || (pl.bytes && !workspace))
     return SSM_ERR_INVALID;
   if (workspace && !aligned(workspace, 16)) return SSM_ERR_ALIGN;
+  if (pl.bytes &&
+      ssm::clash({{workspace, pl.bytes}, writes[0], writes[1], writes[2],
+                  writes[3], writes[4], writes[5]},
+                 reads))
+    return SSM_ERR_INVALID;
   if (gate && dims.batch * dims.heads > 0x7fffffff / pl.groups)
     return SSM_ERR_UNSUPPORTED;
   unsigned char *ws = static_cast<unsigned char *>(workspace);
