@@ -46,8 +46,8 @@
  *     Rows that start on 16-byte boundaries are read 16 bytes at a time.
  *   - float32 results (the states, the decays' gradients, and everything with
  *     float32 activations) are float32-accurate; with bfloat16 activations y,
- *     dq, dk and dv are rounded once at the end and, where no float32 result
- *     depends on it, once for the scores and once for the state they read.
+ *     dq, dk, dv and dlog_decay are off by their rounding at the end and little
+ *     else (what the sums leave out is 2^-16 of a term at most).
  */
 #ifndef SSM_LINATTN_H
 #define SSM_LINATTN_H

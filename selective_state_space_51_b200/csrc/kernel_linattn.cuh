@@ -5,9 +5,10 @@
 // state in front of it:
 //   y_i = si e^{c_i} q_i S + sp sum_{j <= i} e^{c_i - c_j} (q_i . k_j) v_j
 //   S  <- e^{c_C} S + sw sum_j e^{c_C - c_j} k_j (x) v_j
-// A block of four warps owns one head, one tile of 64 value columns and one
-// segment of a sequence: S stays in float32 registers (each warp a quarter of
-// the key rows), the chunk's q, k, v and a bfloat16 copy of S in shared memory.
+// A block of eight warps owns one head, one tile of 64 value columns and one
+// segment of a sequence: S stays in float32 registers (each warp 16 key rows,
+// and half of the columns where there are 64 keys), the chunk's q, k, v and the
+// bfloat16 planes of S in shared memory.
 //
 // The backward pass is three such passes. dq_i reads the same states as y_i,
 // transposed: it is linear attention of (query dy, key v, value k). dk and dv
@@ -23,10 +24,11 @@
 // operands takes the plane pairs (a, b) with a + b < 3; what is left out is
 // below 2^-24 of the product. The state's write takes three planes of the
 // weighted key for both types, so the float32 state has float32 accuracy.
-// Reading the state and the decayed scores takes PS planes: one when only a
-// bfloat16 result comes of them (each then adds a rounding of 2^-9 relative at
-// most half a step, as the result's own rounding does), three for float32
-// results and for the decay's gradient, which sums differences of them.
+// Reading the state and the decayed scores takes PS planes: two where only
+// bfloat16 results come of them (2^-17 of a term is lost, nothing beside the
+// results' rounding; one plane would add as much as that rounding is), three
+// for float32 results and for the decay's gradient, which sums differences of
+// them.
 //
 // Bound by the tensor pipe's mma.sync rate and by what feeds it: six products
 // for float32 operands, at 40% of the pipe's cycles. 64 steps a chunk and 64

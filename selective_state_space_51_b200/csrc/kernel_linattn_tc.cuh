@@ -5,14 +5,15 @@
 //
 // Four products a chunk, each D[128][n] in TMEM:
 //   P  [step i][step j]  = Q K^T            both from shared memory
-//   O1 [step i][value]   = Q S              S: its bfloat16 copy in shared memory
+//   O1 [step i][value]   = Q S              S: a bfloat16 copy in shared memory
 //   U^T[value][key]      = (w V)^T K        (w V)^T from TMEM
 //   O2 [step i][value]   = P' V             P' (decayed scores) from TMEM
 //   y = read_i O1 + O2,  S^T <- keep S^T + U^T (float32, registers)
 // The weighted values need three bfloat16 planes for a float32 state; as the A
 // operand in TMEM they cost no shared memory and no bank traffic, and the
 // state's transpose lies in the same lanes (one value column a lane) as the
-// product that is added to it. They go through two buffers of 32 steps.
+// product that is added to it. The decayed scores and the copy of the state have
+// two planes each, beside which only the result's own rounding is seen.
 //
 // Three warpgroups (a thread has one TMEM lane) share the chunk's 128 weighted
 // steps, which all need the same arithmetic, and have a task of their own
@@ -21,10 +22,10 @@
 // The weighted values pass through three buffers of 32, 32 and 16 steps: the
 // first and the third group have theirs ready while the last chunk's state is
 // still being added up, the second follows once it is. Of the fourth
-// warpgroup, warp 12 moves q, k, v (two chunks deep) and y, 13 issues the
-// products, 14 and 15 sum the decays ahead of their chunks. Everything between
-// them goes through mbarriers with bounded waits; the registers are divided by
-// need.
+// warpgroup, warp 12 moves q, k, v (two chunks deep, but for the q of 128-wide
+// keys and values) and y, 13 issues the products, 14 and 15 sum the decays ahead
+// of their chunks. Everything between them goes through mbarriers with bounded
+// waits; the registers are divided by need.
 //
 // A wait by parity has to come within one phase of its barrier: every wait
 // here is for a phase that cannot be followed by the next before it returns.
@@ -36,11 +37,11 @@
 // at most 1 for decays (no overflow), so a block costs one exponential a row
 // and two products an element. On the diagonal it is formed directly.
 //
-// 148 heads x 8192 steps of (128, 128): 288 us, 4.3 TB/s (0.66 of the copy
+// 148 heads x 8192 steps of (128, 128): 365 us, 3.4 TB/s (0.52 of the copy
 // rate); bound by a chunk's chain (state, its copy, products, weighted values,
-// update: 4.5 us), with 52% of the issue slots and 38% of the tensor pipe busy.
-// Loops unrolled past the instruction cache: 370 us; eight warps doing all of
-// it in turn, 160 heads: 1.1 ms.
+// update: 5.7 us), with 47% of the issue slots and 42% of the tensor pipe busy.
+// With one plane, loops unrolled past the instruction cache took 370 us and
+// short ones 288; eight warps doing all of it in turn, 160 heads, 1.1 ms.
 #pragma once
 
 #include "kernel_linattn.cuh"
@@ -59,8 +60,9 @@ struct Params {
 };
 
 enum Bar {
-  kFull0, kFull1,      // k, v of a stage have arrived
-  kFullQ0, kFullQ1,    // its q
+  kFull0, kFull1,      // k, v (ONE_Q: v) of a stage have arrived
+  kFullQ0, kFullQ1,    // its q (ONE_Q: the first of them alone)
+  kFullK0, kFullK1,    // ONE_Q: its k
   kEmpty0, kEmpty1,    // the stage's products are done
   kScores,             // P
   kRead,               // O1
@@ -113,29 +115,53 @@ __host__ __device__ constexpr int slot_buffer(int s) {
   return s < 3 ? s : s == 3 ? 0 : 2;
 }
 
-template <int QD, int TV, int PS, bool STATE_ONLY>
+// Planes of the decayed scores and of the state that is read. One of each adds
+// a rounding as large as the result's own (prompts: 2.34e-3 off, where the last
+// rounding alone makes 1.66e-3); with two the rest is not seen beside it. They
+// cost 148 heads x 8192 steps of (128, 128) 281 -> 365 us: the state's second
+// copy is on the chunk's chain, and there is more code than the instruction
+// cache holds (4 times the misses).
+constexpr int PS = 2;
+
+template <int QD, int TV, bool STATE_ONLY>
 struct Lay {
   static constexpr int Q = kChunk * QD * 2, V = kChunk * TV * 2;
-  static constexpr int STAGE = (STATE_ONLY ? Q : 2 * Q) + V;  // k, v(, q)
-  static constexpr int S = 2 * STAGE;
-  // y: in the place of the chunk's q where there is no room of its own
-  static constexpr bool OVER_Q = QD == 128 && TV == 128;
+  // Two stages of q, k, v and two planes of the state are more than there is
+  // where both sizes are 128: one q then, which is loaded once its forerunner
+  // has been multiplied with the state, and y in the place of the chunk's k.
+  static constexpr bool ONE_Q = QD == 128 && TV == 128 && !STATE_ONLY;
+  static constexpr int STAGE = (STATE_ONLY || ONE_Q ? Q : 2 * Q) + V;
+  static constexpr int Q0 = ONE_Q ? 2 * STAGE : Q + V;  // (of a stage: k, v, q)
+  static constexpr int S = 2 * STAGE + (ONE_Q ? Q : 0);
   static constexpr int Y = S + (STATE_ONLY ? 0 : PS * TV * QD * 2);
-  static constexpr int GATES = Y + (STATE_ONLY || OVER_Q ? 0 : V);
+  static constexpr int GATES = Y + (STATE_ONLY || ONE_Q ? 0 : V);
   static constexpr int BYTES = GATES + int(sizeof(Gates));
   // TMEM columns
   static constexpr uint32_t P = 0, O = 128, U = 256, W = 384;
 };
+
+// Two planes of a pair of floats, the first cut off (exact to subtract, and no
+// conversion), the second rounded: 2^-16 of the value at most is lost.
+__device__ __forceinline__ void planes(float2 x, uint32_t (&p)[PS]) {
+  static_assert(PS == 2, "");
+  const uint32_t a = __float_as_uint(x.x), b = __float_as_uint(x.y);
+  p[0] = __byte_perm(a, b, 0x7632);
+  const float2 r = fma2(make_float2(__uint_as_float(a & 0xffff0000u),
+                                    __uint_as_float(b & 0xffff0000u)),
+                        make_float2(-1.0f, -1.0f), x);
+  p[1] = la::pack2(r.x, r.y);
+}
 
 // A 16-byte group of a 128-byte row in the 128-byte swizzle.
 __device__ __forceinline__ int swizzled(int row, int group) {
   return row * 128 + ((group ^ (row % 8)) * 16);
 }
 
-template <int QD, int TV, int PS, bool STATE_ONLY>
+template <int QD, int TV, bool STATE_ONLY>
 __global__ void __launch_bounds__(kThreads, 1)
     linattn_tc_kernel(const __grid_constant__ Params pp) {
-  using L_ = Lay<QD, TV, PS, STATE_ONLY>;
+  using L_ = Lay<QD, TV, STATE_ONLY>;
+  constexpr bool ONE_Q = L_::ONE_Q;
   using la::bf16;
   using la::pack2;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -260,6 +286,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::bar_arrive(bar(kWeighed + slot));
     return true;
   };
+  // The barrier of chunk `it`'s q, and how often it has been used.
+  auto q_full = [&](int it) {
+    return ONE_Q ? int(kFullQ0) : kFullQ0 + (it & 1);
+  };
+  auto q_use = [&](int it) { return ONE_Q ? it : it / 2; };
   // Whether chunk `it`'s values and weights are there.
   auto chunk_in = [&](int it) {
     return wait(kFull0 + (it & 1), it / 2) &&
@@ -276,8 +307,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int qh = h / (p.heads / job.q_heads);
       const int vh = h / (p.heads / job.v_heads);
       const bool staged = !STATE_ONLY && !job.y_f32;
-      // k and v come as soon as their stage's products are done; q, where y is
-      // staged in its place, once y has been read
+      // k and v come as soon as their stage's products are done. With one q, k
+      // comes once the y in its place has been read, and q after its
+      // forerunner's last product; both are brought to L2 before.
       int it = 0;
 #pragma unroll 1
       for (; fit && it < n_live + 2; ++it) {
@@ -286,11 +318,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (it < n_live) {
           if (it >= 2 && !wait(kEmpty0 + st, it / 2 - 1)) break;
           if (lane == 0) {
-            tc::bar_expect(f, L_::Q + L_::V);
+            tc::bar_expect(f, ONE_Q ? L_::V : L_::Q + L_::V);
 #pragma unroll 1
             for (int c = 0; c < QD / 64; ++c)
-              tc::load_box(s + c * 16384, &maps[1], f, c * 64, kh, low(it),
-                           int(b));
+              if constexpr (ONE_Q) {
+                tc::prefetch_box(&maps[1], c * 64, kh, low(it), int(b));
+                tc::prefetch_box(&maps[0], c * 64, qh, low(it), int(b));
+              } else {
+                tc::load_box(s + c * 16384, &maps[1], f, c * 64, kh, low(it),
+                             int(b));
+              }
 #pragma unroll 1
             for (int c = 0; c < TV / 64; ++c)
               tc::load_box(s + L_::Q + c * 16384, &maps[2], f, c * 64, vh,
@@ -302,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (it >= 2 && staged) {
           if (!wait(kStaged, it - 2)) break;
           if (lane == 0) {
-            const uint32_t y = L_::OVER_Q ? s + L_::Q + L_::V : base + L_::Y;
+            const uint32_t y = ONE_Q ? s : base + L_::Y;
 #pragma unroll 1
             for (int c = 0; c * 64 < job.vd; ++c)
               tc::store_box(&maps[3], y + c * 16384, c * 64, h, low(it - 2),
@@ -312,12 +349,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        if (it < n_live && lane == 0) {
-          tc::bar_expect(bar(kFullQ0 + st), L_::Q);
+        if (it >= n_live) continue;
+        if constexpr (ONE_Q) {
+          if (lane == 0) {
+            tc::bar_expect(bar(kFullK0 + st), L_::Q);
+#pragma unroll 1
+            for (int c = 0; c < QD / 64; ++c)
+              tc::load_box(s + c * 16384, &maps[1], bar(kFullK0 + st), c * 64,
+                           kh, low(it), int(b));
+          }
+          __syncwarp();
+          if (it > 0 && !wait(kRead, it - 1)) break;
+        }
+        if (lane == 0) {
+          const uint32_t q = ONE_Q ? base : s, fq = bar(q_full(it));
+          tc::bar_expect(fq, L_::Q);
 #pragma unroll 1
           for (int c = 0; c < QD / 64; ++c)
-            tc::load_box(s + L_::Q + L_::V + c * 16384, &maps[0],
-                         bar(kFullQ0 + st), c * 64, qh, low(it), int(b));
+            tc::load_box(q + L_::Q0 + c * 16384, &maps[0], fq, c * 64, qh,
+                         low(it), int(b));
         }
         __syncwarp();
       }
@@ -330,8 +380,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int i = 0; i < 1 << 12; ++i)
             if (tc::bar_try(bar(kFull0 + (it & 1)), uint32_t(it / 2) & 1u) &&
-                (STATE_ONLY || tc::bar_try(bar(kFullQ0 + (it & 1)),
-                                           uint32_t(it / 2) & 1u)))
+                (STATE_ONLY ||
+                 tc::bar_try(bar(q_full(it)), uint32_t(q_use(it)) & 1u)) &&
+                (!ONE_Q || tc::bar_try(bar(kFullK0 + (it & 1)),
+                                       uint32_t(it / 2) & 1u)))
               break;
       }
     } else if (warp == 13) {
@@ -346,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t stage0 = tc::operand(base, 16384);
       const uint64_t state0 = tc::operand(base + L_::S, 0);
       constexpr uint64_t kStage = L_::STAGE / 16, kV = L_::Q / 16,
-                         kQ = (L_::Q + L_::V) / 16;
+                         kQ = L_::Q0 / 16;
       bool alive = fit;
       // round i: chunk i - 1's update, reading and output, then chunk i's
       // scores, which are decayed while the state is brought up to date
@@ -354,7 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i <= n_live && alive; ++i) {
         if (i > 0) {
           const int it = i - 1, st = it & 1;
-          const uint64_t K = stage0 + st * kStage, V = K + kV, Q = K + kQ;
+          const uint64_t K = stage0 + st * kStage, V = K + kV,
+                         Q = (ONE_Q ? stage0 : K) + kQ;
           alive = wait(kState, it);
           // the state's update first: the next chunk waits for it
 #pragma unroll 1
@@ -412,9 +465,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (i < n_live) {
           const int st = i & 1;
-          const uint64_t K = stage0 + st * kStage, Q = K + kQ;
+          const uint64_t K = stage0 + st * kStage,
+                         Q = (ONE_Q ? stage0 : K) + kQ;
           alive = wait(kFull0 + st, i / 2) &&
-                  (STATE_ONLY || wait(kFullQ0 + st, i / 2)) &&
+                  (!ONE_Q || wait(kFullK0 + st, i / 2)) &&
+                  (STATE_ONLY || wait(q_full(i), q_use(i))) &&
                   (i != ragged || wait(kClean, 0));
           if (!alive) break;
           tc::after_sync();
@@ -572,8 +627,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           uint32_t pl[PS];
-          la::split2<PS>(__uint_as_float(v[2 * i]),
-                         __uint_as_float(v[2 * i + 1]), pl);
+          planes(make_float2(__uint_as_float(v[2 * i]),
+                             __uint_as_float(v[2 * i + 1])),
+                 pl);
 #pragma unroll
           for (int s = 0; s < PS; ++s) w[s][i] = pl[s];
         }
@@ -599,11 +655,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; i += 4) {
             const float4 f =
                 *reinterpret_cast<const float4 *>(gt.near + nb * 32 + i);
-            const float d[4] = {f.x, f.y, f.z, f.w};
+            const float2 d[2] = {make_float2(f.x, f.y),
+                                 make_float2(f.z, f.w)};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              v[i + j] =
-                  __float_as_uint(__uint_as_float(v[i + j]) * (e * d[j]));
+            for (int j = 0; j < 2; ++j) {
+              const float2 x =
+                  mul2(make_float2(__uint_as_float(v[i + 2 * j]),
+                                   __uint_as_float(v[i + 2 * j + 1])),
+                       mul2(make_float2(e, e), d[j]));
+              v[i + 2 * j] = __float_as_uint(x.x);
+              v[i + 2 * j + 1] = __float_as_uint(x.y);
+            }
           }
           put(nb * 32, v);
           put(nb * 32 + 16, v + 16);
@@ -663,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       SF +
                   r % kLaTile
             : nullptr;
-    float S[QD];
+    float2 S[QD / 2];
     {
       const float *src = nullptr;
       int keys = 0;
@@ -679,7 +741,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!src) keys = 0;
 #pragma unroll
       for (int i = 0; i < QD; ++i) {
-        S[i] = i < keys ? *src : 0.0f;
+        const float x = i < keys ? *src : 0.0f;
+        (i % 2 ? S[i / 2].y : S[i / 2].x) = x;
         src += stride;
       }
     }
@@ -687,18 +750,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto put_state = [&]() {
       if constexpr (!STATE_ONLY) {
         if (r < TV) {
+          // (the swizzle of a row's first group; the others are 16 bytes times
+          // their number away, without carries)
+          const uint32_t at = base + L_::S + swizzled(r, 0);
 #pragma unroll
           for (int i = 0; i < QD; i += 8) {
             uint32_t w[4][PS];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              la::split2<PS>(S[i + 2 * j], S[i + 2 * j + 1], w[j]);
-            unsigned char *dst = smem + L_::S + (i / 64) * TV * 128 +
-                                 swizzled(r, i % 64 / 8);
+            for (int j = 0; j < 4; ++j) planes(S[i / 2 + j], w[j]);
+            const uint32_t dst = at ^ uint32_t(i % 64 / 8 * 16);
 #pragma unroll
             for (int s = 0; s < PS; ++s)
-              *reinterpret_cast<uint4 *>(dst + s * TV * QD * 2) =
-                  make_uint4(w[0][s], w[1][s], w[2][s], w[3][s]);
+              tc::smem_st4(dst + (i / 64) * TV * 128 + s * TV * QD * 2,
+                           w[0][s], w[1][s], w[2][s], w[3][s]);
           }
         }
         tc::fence_async();
@@ -717,6 +781,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         alive = weigh(it, slot);
       if (alive && it + 1 < n_live) {
         alive = chunk_in(it + 1);
+        if (ONE_Q && alive && it + 1 == ragged)
+          alive = wait(kFullK0 + ((it + 1) & 1), (it + 1) / 2);
         if (alive && it + 1 == ragged) {
           // rows behind the sequence's end: zeros, whatever was loaded
           unsigned char *Ks = smem + ((it + 1) & 1) * L_::STAGE,
@@ -748,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::after_sync();
       if (keep == 0.0f) {  // a restart forgets the state whatever it held
 #pragma unroll
-        for (int i = 0; i < QD; ++i) S[i] = 0.0f;
+        for (int i = 0; i < QD / 2; ++i) S[i] = make_float2(0.0f, 0.0f);
       }
 #pragma unroll
       for (int u = 0; u < QD; u += 32) {
@@ -756,8 +822,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_ld32(mine + L_::U + u, t);
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          S[u + i] = fmaf(keep, S[u + i], __uint_as_float(t[i]));
+        for (int i = 0; i < 16; ++i)
+          S[u / 2 + i] = fma2(make_float2(keep, keep), S[u / 2 + i],
+                              make_float2(__uint_as_float(t[2 * i]),
+                                          __uint_as_float(t[2 * i + 1])));
       }
       put_state();
     }
@@ -777,13 +845,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (rev && len > 0) {
         const float f = la::decay_of(la::gate_at<bf16>(p, b, 0, h));
 #pragma unroll
-        for (int i = 0; i < QD; ++i) S[i] = f == 0.0f ? 0.0f : S[i] * f;
+        for (int i = 0; i < QD / 2; ++i)
+          S[i] = f == 0.0f ? make_float2(0.0f, 0.0f)
+                           : mul2(S[i], make_float2(f, f));
       }
     }
     if (!alive || !dst) keys = 0;
 #pragma unroll
     for (int i = 0; i < QD; ++i) {
-      if (i < keys) *dst = S[i];
+      if (i < keys) *dst = i % 2 ? S[i / 2].y : S[i / 2].x;
       dst += stride;
     }
   } else {
@@ -851,8 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (staged && it > 0 && !wait(kStored, it - 1)) break;
         if (!wait(kOut, it)) break;
         tc::after_sync();
-        unsigned char *ys =
-            smem + (L_::OVER_Q ? st * L_::STAGE + L_::Q + L_::V : L_::Y);
+        unsigned char *ys = smem + (ONE_Q ? st * L_::STAGE : L_::Y);
         const int64_t row = (b * L + t) * p.heads + h;
         float dot = 0.0f;
         // (the flags are read in the loop, so that it stays one loop)

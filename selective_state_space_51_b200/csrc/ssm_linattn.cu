@@ -234,8 +234,8 @@ int run_jobs(const LaParams &p, int n, int dtype, bool exact, cudaStream_t s) {
   if (exact)
     return qd == 64 ? launch_jobs<bf16, 1, 3, 64>(p, n, s)
                     : launch_jobs<bf16, 1, 3, 128>(p, n, s);
-  return qd == 64 ? launch_jobs<bf16, 1, 1, 64>(p, n, s)
-                  : launch_jobs<bf16, 1, 1, 128>(p, n, s);
+  return qd == 64 ? launch_jobs<bf16, 1, 2, 64>(p, n, s)
+                  : launch_jobs<bf16, 1, 2, 128>(p, n, s);
 }
 
 // ---- the tensor-memory kernel
@@ -278,14 +278,14 @@ bool tc_takes(const ssm_linattn_dims &d, int dtype, const void *q,
   return true;
 }
 
-template <int QD, int TV, int PS>
+template <int QD, int TV>
 int launch_tc(const ssm::lat::Params &pp, int n, cudaStream_t s) {
   const LaParams &p = pp.p;
   const int64_t one = p.bhs;
   if (one > 0x7fffffff / p.nseg) return SSM_ERR_UNSUPPORTED;
   if (p.nseg > 1) {
-    auto kern = ssm::lat::linattn_tc_kernel<QD, TV, 1, true>;
-    constexpr int smem = ssm::lat::Lay<QD, TV, 1, true>::BYTES;
+    auto kern = ssm::lat::linattn_tc_kernel<QD, TV, true>;
+    constexpr int smem = ssm::lat::Lay<QD, TV, true>::BYTES;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem < kOnePerSm ? kOnePerSm : smem) !=
         cudaSuccess) {
@@ -300,8 +300,8 @@ int launch_tc(const ssm::lat::Params &pp, int n, cudaStream_t s) {
     join<QD>(p, n, tiles, s);
     if (cudaGetLastError() != cudaSuccess) return SSM_ERR_CUDA;
   }
-  auto kern = ssm::lat::linattn_tc_kernel<QD, TV, PS, false>;
-  constexpr int need = ssm::lat::Lay<QD, TV, PS, false>::BYTES;
+  auto kern = ssm::lat::linattn_tc_kernel<QD, TV, false>;
+  constexpr int need = ssm::lat::Lay<QD, TV, false>::BYTES;
   constexpr int smem = need < kOnePerSm ? kOnePerSm : need;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            smem) != cudaSuccess) {
@@ -312,14 +312,8 @@ int launch_tc(const ssm::lat::Params &pp, int n, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
 
-// Two planes of the state and the scores do not fit beside two 128-wide
-// stages.
-bool tc_exact_fits(int64_t key, int64_t value) {
-  return key <= 64 || value <= 64;
-}
-
-// The jobs of `p` (n of them), which share their sizes and PS.
-int run_tc(const LaParams &p, int n, bool exact, int device, cudaStream_t s) {
+// The jobs of `p` (n of them), which share their sizes.
+int run_tc(const LaParams &p, int n, int device, cudaStream_t s) {
   ssm::lat::Params pp{};
   pp.p = p;
   pp.status = status_word(device);
@@ -338,14 +332,10 @@ int run_tc(const LaParams &p, int n, bool exact, int device, cudaStream_t s) {
       return SSM_ERR_CUDA;
   }
   const bool q64 = p.job[0].qd <= 64, v64 = p.job[0].vd <= 64;
-  if (exact)
-    return q64 ? (v64 ? launch_tc<64, 64, 2>(pp, n, s)
-                      : launch_tc<64, 128, 2>(pp, n, s))
-               : launch_tc<128, 64, 2>(pp, n, s);
-  return q64 ? (v64 ? launch_tc<64, 64, 1>(pp, n, s)
-                    : launch_tc<64, 128, 1>(pp, n, s))
-             : (v64 ? launch_tc<128, 64, 1>(pp, n, s)
-                    : launch_tc<128, 128, 1>(pp, n, s));
+  return q64 ? (v64 ? launch_tc<64, 64>(pp, n, s)
+                    : launch_tc<64, 128>(pp, n, s))
+             : (v64 ? launch_tc<128, 64>(pp, n, s)
+                    : launch_tc<128, 128>(pp, n, s));
 }
 
 // Every token's rows of a tensor, from the first element to the last.
@@ -483,12 +473,12 @@ int ssm_linattn_fwd(int device, const void *q, const void *k, const void *v,
     first.nseg = 1;
     first.seg_len = pl.whole_len;
     first.bhs = int(pl.whole);
-    rc = run_tc(first, 1, false, device, s);
+    rc = run_tc(first, 1, device, s);
     if (rc != SSM_OK) return rc;
     p.bh0 = int(pl.whole);
     p.bhs -= int(pl.whole);
   }
-  return run_tc(p, 1, false, device, s);
+  return run_tc(p, 1, device, s);
 }
 
 int ssm_linattn_step(int device, const void *q, const void *k, const void *v,
@@ -598,8 +588,7 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
   // the two planes that fit beside the stages there leave it 5.6e-5 off (8192
   // steps of long memory), the other kernel's three planes 1e-6.
   const Path path = tc_takes(dims, dtype, q, k, v, {dy, dq, dk, dv}) &&
-                            !dhead_log_decay &&
-                            (!gate || tc_exact_fits(dims.dv, dims.dk))
+                            !dhead_log_decay
                         ? Path::kTc
                         : Path::kAny;
   const Plan pl = plan_bwd(dims, path, gate, sms);
@@ -674,7 +663,7 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
   const bool one = (K <= ssm::kLaTile) == (V <= ssm::kLaTile);
   p.job[2] = jv;
   auto run = [&](int n, bool exact) {
-    return path == Path::kTc ? run_tc(p, n, exact, device, s)
+    return path == Path::kTc ? run_tc(p, n, device, s)
                              : run_jobs(p, n, dtype, exact, s);
   };
   rc = run(one ? 3 : 2, gate);

@@ -12,6 +12,13 @@ __device__ __forceinline__ uint32_t smem_addr(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+__device__ __forceinline__ void smem_st4(uint32_t addr, uint32_t a, uint32_t b,
+                                         uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a),
+               "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
 // ---- mbarriers
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar),
@@ -212,6 +219,14 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map,
       "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::"
       "bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
       "l"(map), "r"(bar), "r"(x), "r"(head), "r"(token), "r"(batch)
+      : "memory");
+}
+__device__ __forceinline__ void prefetch_box(const CUtensorMap *map, int x,
+                                             int head, int token, int batch) {
+  asm volatile(
+      "cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, "
+      "%4}];" ::"l"(map),
+      "r"(x), "r"(head), "r"(token), "r"(batch)
       : "memory");
 }
 __device__ __forceinline__ void store_box(const CUtensorMap *map, uint32_t src,
