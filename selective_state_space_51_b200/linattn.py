@@ -161,8 +161,11 @@ class LinearAttention:
     def sync_status(self, stream=None) -> int:
         """Waits for the stream; SSM_OK unless a kernel's bounded wait gave
         up or the device has an error."""
-        return launch(self._torch, self.device, stream, lambda s: ssm_linattn_sync_status(
-            self.device.index, s))
+        torch = self._torch
+        with torch.cuda.device(self.device):
+            if stream is None:
+                stream = torch.cuda.current_stream()
+            return ssm_linattn_sync_status(self.device.index, stream)
 
     def __call__(self, q, k, v, log_decay=None, head_log_decay=None,
                  scale=None, lengths=None, h0=None, y=None, h_last=None,

@@ -102,3 +102,20 @@ def test_captured_on_a_stream_of_its_own(ops, data):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(alone, want))
+
+
+def test_the_status_waits_for_its_own_stream(ops):
+    """Not for the current one (unless that is the default stream, which the
+    status word is read on)."""
+    side, here = torch.cuda.Stream(), torch.cuda.Stream()
+    done = torch.cuda.Event()
+    assert ops[0].sync_status(stream=side) == S.SSM_OK    # (first use)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(here):
+        torch.cuda._sleep(10 * SLEEP)
+        done.record()
+        for s in (side, side.cuda_stream):
+            assert ops[0].sync_status(stream=s) == S.SSM_OK
+        assert not done.query()
+        assert ops[0].sync_status() == S.SSM_OK
+        assert done.query()
