@@ -39,6 +39,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <math_constants.h>
 #include <stdint.h>
 
 #include "device_math.cuh"
@@ -227,7 +228,8 @@ struct alignas(16) Gates {
   int from[kLaChunk];                // the last restart at or before step i
   float read[kLaChunk];              // e^{c_i}, 0 behind a restart
   float write[kLaChunk];             // e^{c_C - c_i}, 0 before a restart
-  float keep;                        // e^{c_C}, 0 with a restart
+  float2 keep;                       // of e^{c_C} (see keep_of), 0 with a restart
+  double end;                        // c_C, -infinity with a restart
 };
 
 // 2^x for a 64-bit x: the float32 rounding of x is put back to first order.
@@ -236,6 +238,19 @@ __device__ __forceinline__ float ex2_d(double x) {
   if (x < -126.0) return 0.0f;
   const float hi = float(x);
   return ex2(hi) * fmaf(float(x - double(hi)), kLn2, 1.0f);
+}
+
+// What is kept of a state over a chunk, 2^x, as {m, b}: S <- b S + (m S + ...).
+// A kept part near 1 is {2^x - 1, 1}: rounded as one number it would be off by
+// up to 2^-24, always to the same side where a head's decay is the same for
+// every step, which over the 1600 chunks that a decay of e^-0.00001 a step lets
+// through made 1e-5 of the state.
+__device__ __forceinline__ float2 keep_of(double x) {
+  return x > -1.0 ? make_float2(expm1f(float(x * 0.6931471805599453)), 1.0f)
+                  : make_float2(ex2_d(x), 0.0f);
+}
+__device__ __forceinline__ bool none_kept(float2 keep) {
+  return keep.x == 0.0f && keep.y == 0.0f;
 }
 
 // The decay of one step, from its log decay.
@@ -305,7 +320,10 @@ __device__ __forceinline__ void load_gates(Gates &g, const LaParams &p,
     g.read[r] = from[j] < 0 ? ex2_d(c[j]) : 0.0f;
     g.write[r] = r >= end_r ? ex2_d(end - c[j]) : 0.0f;
   }
-  if (lane == 0) g.keep = end_r < 0 ? ex2_d(end) : 0.0f;
+  if (lane == 0) {
+    g.keep = end_r < 0 ? keep_of(end) : make_float2(0.0f, 0.0f);
+    g.end = end_r < 0 ? end : -CUDART_INF;
+  }
 }
 
 template <typename T, int NP, int PS, int QD, bool STATE_ONLY>
@@ -434,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
     }
   }
 
-  float seg_keep = 1.0f;
+  double seg_sum = 0.0;  // of the chunks' log decays
   const int chunks = int(p.seg_len / kLaChunk);
   auto rows_of = [&](int ch) {
     Rows rows;
@@ -761,8 +779,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
                     job.reverse);
 
     // ---- the state: S <- keep S + (weighted k)^T v
-    const float keep = gt.keep;
-    seg_keep *= keep;
+    const float2 keep = gt.keep;
+    if constexpr (STATE_ONLY) seg_sum += gt.end;
     float U[NT][4], lo[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -819,7 +837,9 @@ __global__ void __launch_bounds__(kThreads, MINB)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float u = U[n][j] + lo[n][j];
-        S[n][j] = keep == 0.0f ? u : fmaf(keep, S[n][j], u);
+        S[n][j] = none_kept(keep)
+                      ? u
+                      : fmaf(keep.y, S[n][j], fmaf(keep.x, S[n][j], u));
       }
   }
 
@@ -829,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
           make_float2(S[n][2 * hr], S[n][2 * hr + 1]);
     });
     if (tile == 0 && threadIdx.x == 0)
-      job.seg_decay[int64_t(local) * p.nseg + seg] = seg_keep;
+      job.seg_decay[int64_t(local) * p.nseg + seg] = exp2(seg_sum);
   } else if (job.last && seg == p.nseg - 1) {
     // running backwards, the first token's own decay is still to come
     float f = 1.0f;
@@ -849,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
 
 // The states in front of the segments, from what each segment adds on its own:
 // S_{m+1} = decay_m S_m + U_m, in place (entry m takes S_m; the last segment's
-// own part is not formed here). One thread per state element.
+// own part is not formed here), in 64 bits. One thread per state element.
 template <int QD>
 __global__ void __launch_bounds__(256)
     linattn_join_kernel(const __grid_constant__ LaParams p) {
@@ -862,16 +882,17 @@ __global__ void __launch_bounds__(256)
             col = el % kLaTile + tile * kLaTile;
   for (int64_t local = blockIdx.y; local < p.bhs; local += gridDim.y) {
     const int64_t bh = p.bh0 + local;
-    float S = 0.0f;
+    double S = 0.0;
     if (job.init && row < job.qd && col < job.vd)
       S = job.init[bh * job.qd * job.vd + int64_t(row) * job.state_rs +
                    int64_t(col) * job.state_cs];
     float *u = job.seg_state + local * p.nseg * per + el;  // (a segment: per)
-    const float *d = job.seg_decay + local * p.nseg;
+    const double *d = job.seg_decay + local * p.nseg;
     // sixteen segments' parts are on their way at a time
     const int n = p.nseg - 1;
     for (int m = 0; m < n; m += 16) {
-      float a[16], k[16];
+      float a[16];
+      double k[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j)
         if (m + j < n) {
@@ -881,11 +902,11 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int j = 0; j < 16; ++j)
         if (m + j < n) {
-          u[int64_t(m + j) * per] = S;
-          S = k[j] == 0.0f ? a[j] : fmaf(k[j], S, a[j]);
+          u[int64_t(m + j) * per] = float(S);
+          S = k[j] == 0.0 ? double(a[j]) : fma(k[j], S, double(a[j]));
         }
     }
-    u[int64_t(n) * per] = S;
+    u[int64_t(n) * per] = float(S);
   }
 }
 

@@ -95,7 +95,8 @@ struct Gates {
   float write[2][kChunk];        // sw e^{c_C - c_i}, 0 before a restart
   unsigned short lo[kChunk];     // (bfloat16)
   unsigned char from[kChunk];    // the last restart at or before the step
-  float keep[2];                 // e^{c_C}, 0 with a restart
+  float2 keep[2];                // of e^{c_C} (la::keep_of), 0 with a restart
+  double end[2];                 // c_C, -infinity with a restart
   int staged, dotted;            // what becomes of y (see the third group)
   int dead;
   uint32_t tmem;
@@ -576,7 +577,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           gt.write[par][row] =
               s >= end_r ? ex2(float(end - pick(j, c))) * job.sw : 0.0f;
         }
-        if (lane == 0) gt.keep[par] = end_r < 0 ? ex2(float(end)) : 0.0f;
+        if (lane == 0) {
+          gt.keep[par] =
+              end_r < 0 ? la::keep_of(end) : make_float2(0.0f, 0.0f);
+          if (STATE_ONLY) gt.end[par] = end_r < 0 ? end : -CUDART_INF;
+        }
         __syncwarp();
         if (lane == 0) tc::bar_arrive(bar(kWeights0 + par));
         if constexpr (!STATE_ONLY) {
@@ -770,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::before_sync();
       tc::bar_arrive(bar(kState));
     };
-    float seg_keep = 1.0f;
+    double seg_sum = 0.0;  // of the chunks' log decays
     put_state();
     bool alive = fit;
     // In turn: the slots of chunk it, the arrival of chunk it + 1, the update.
@@ -806,13 +811,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!alive) break;
       if (it < 0) continue;
-      const float keep = gt.keep[it & 1];
-      seg_keep *= keep;
+      const float2 keep = gt.keep[it & 1];
+      if (STATE_ONLY) seg_sum += gt.end[it & 1];
       tc::bar_arrive(bar(kWeightsFree0 + (it & 1)));
       alive = wait(kUpdate, it);
       if (!alive) break;
       tc::after_sync();
-      if (keep == 0.0f) {  // a restart forgets the state whatever it held
+      if (la::none_kept(keep)) {  // a restart forgets whatever it held
 #pragma unroll
         for (int i = 0; i < QD / 2; ++i) S[i] = make_float2(0.0f, 0.0f);
       }
@@ -823,9 +828,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          S[u / 2 + i] = fma2(make_float2(keep, keep), S[u / 2 + i],
-                              make_float2(__uint_as_float(t[2 * i]),
-                                          __uint_as_float(t[2 * i + 1])));
+          S[u / 2 + i] =
+              fma2(make_float2(keep.y, keep.y), S[u / 2 + i],
+                   fma2(make_float2(keep.x, keep.x), S[u / 2 + i],
+                        make_float2(__uint_as_float(t[2 * i]),
+                                    __uint_as_float(t[2 * i + 1]))));
       }
       put_state();
     }
@@ -836,7 +843,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (STATE_ONLY) {
       dst = seg_state;
       keys = QD;
-      if (r == 0) job.seg_decay[int64_t(local) * p.nseg + seg] = seg_keep;
+      if (r == 0)
+        job.seg_decay[int64_t(local) * p.nseg + seg] = exp2(seg_sum);
     } else if (job.last && seg == p.nseg - 1 && r < job.vd) {
       dst = job.last + bh * job.qd * job.vd + int64_t(r) * job.state_cs;
       keys = job.qd;

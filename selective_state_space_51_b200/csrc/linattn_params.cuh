@@ -37,7 +37,7 @@ struct LaJob {
   float *rows;                           // [2 tiles, b, heads, L] row dots,
                                          // of 32 columns each
   float *seg_state;                      // [bhs, nseg, tiles, QD, 64]
-  float *seg_decay;                      // [bhs, nseg]
+  double *seg_decay;                     // [bhs, nseg]
   float *anchor;                         // [b, heads, anchors, tiles, QD, 64]
                                          // or nullptr: the state in front of
                                          // every kLaAnchor-th token

@@ -139,7 +139,7 @@ Plan plan_fwd(const ssm_linattn_dims &d, Path path, int sms) {
     const size_t bh = size_t(all - pl.whole);
     pl.state[0] = take(&pl.bytes, bh * pl.nseg * tiles * key_pad(d.dk) *
                                       ssm::kLaTile);
-    pl.decay[0] = take(&pl.bytes, bh * pl.nseg);
+    pl.decay[0] = take(&pl.bytes, bh * pl.nseg * 2);  // 64-bit
   }
   return pl;
 }
@@ -157,7 +157,7 @@ Plan plan_bwd(const ssm_linattn_dims &d, Path path, bool gate, int sms) {
       pl.state[j] = take(&pl.bytes, bh * pl.nseg * (j < 2 ? tk : tv) *
                                         key_pad(j < 2 ? d.dv : d.dk) *
                                         ssm::kLaTile);
-      pl.decay[j] = take(&pl.bytes, bh * pl.nseg);
+      pl.decay[j] = take(&pl.bytes, bh * pl.nseg * 2);  // 64-bit
     }
   if (d.groups != d.heads) {
     pl.part_dq = take(&pl.bytes, bh * d.seqlen * d.dk);
@@ -464,7 +464,7 @@ int ssm_linattn_fwd(int device, const void *q, const void *k, const void *v,
   j.sp = j.si = scale; j.sw = 1.0f;
   if (pl.nseg > 1) {
     j.seg_state = reinterpret_cast<float *>(ws + pl.state[0]);
-    j.seg_decay = reinterpret_cast<float *>(ws + pl.decay[0]);
+    j.seg_decay = reinterpret_cast<double *>(ws + pl.decay[0]);
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (path == Path::kAny) return run_jobs(p, 1, dtype, false, s);
@@ -641,7 +641,7 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
     LaJob *all[3] = {&jq, &jk, &jv};
     for (int i = 0; i < 3; ++i) {
       all[i]->seg_state = at(pl.state[i]);
-      all[i]->seg_decay = at(pl.decay[i]);
+      all[i]->seg_decay = reinterpret_cast<double *>(ws + pl.decay[i]);
     }
   }
   if (gate) {

@@ -1,0 +1,44 @@
+"""States that remember tens of thousands of steps: the kept part of a state
+is multiplied hundreds of times, and what it is rounded by must not add up.
+
+With u = 2^-24: a chunk's update rounds the state once or twice, to either side
+(0.3 u, the root mean square of a rounding to nearest), so n chunks leave
+0.6 u sqrt(n); the products in front of it are 8 u off whatever n is (truncated
+sums of 16 products and the weights' exponentials). Twice that is allowed:
+u (16 + 1.2 sqrt(n)). A kept part that were off by 0.3 u to the same side each
+time would make 0.3 u n / 2."""
+import numpy as np
+import pytest
+
+import mixer_oracle as M
+import selective_state_space_51_b200 as S
+from test_gpu_linattn import Case, host
+
+pytestmark = pytest.mark.gpu
+L = 40_000
+
+
+@pytest.fixture(scope="module")
+def attn():
+    return S.LinearAttention(0)
+
+
+def rel(got, ref):
+    return np.linalg.norm(got - ref) / np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("heads", [4, 148])        # cut into segments, and not
+@pytest.mark.parametrize("decay", [1e-5, 1e-4, -2e-5])
+def test_long_memory(attn, dtype, heads, decay):
+    c = Case(dtype, 1, L, heads, heads, 8, 8, gate="head", state=True)
+    rng = np.random.default_rng(3)
+    c.head = (-decay * (0.5 + rng.random(heads))).astype(
+        np.float32).astype(np.float64)
+    ref_y, ref_h = M.forward(c.q, c.k, c.v, c.g, c.scale, c.h0)
+    y, h = c.run(attn)
+    tol = 2.0 ** -24 * (16 + 1.2 * np.sqrt(L / 64))
+    print("h %.2f of its bound" % (rel(host(h), ref_h) / tol))
+    assert rel(host(h), ref_h) <= tol
+    if dtype == "f32":
+        assert rel(host(y), ref_y) <= tol
