@@ -1157,7 +1157,8 @@ __global__ void __launch_bounds__(256)
   if (p.log_decay)
     gd = double(to_f(static_cast<const T *>(p.log_decay)[bh]));
   if (p.head_log_decay) gd += double(p.head_log_decay[h]);
-  const float a = decay_of(gd);
+  const float2 a = gd < kRestart ? make_float2(0.0f, 0.0f)
+                                 : keep_of(gd * 1.4426950408889634);
   float v[W], y[W];
 #pragma unroll
   for (int j = 0; j < W; ++j) {
@@ -1175,7 +1176,10 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int j = 0; j < W; ++j) {
         // a = 0 starts anew, whatever the state held
-        x[i][j] = a == 0.0f ? ks[r] * v[j] : fmaf(a, x[i][j], ks[r] * v[j]);
+        const float kv = ks[r] * v[j];
+        x[i][j] = none_kept(a)
+                      ? kv
+                      : fmaf(a.y, x[i][j], fmaf(a.x, x[i][j], kv));
         y[j] = fmaf(qs[r], x[i][j], y[j]);
       }
       float *s = S + int64_t(r) * p.dv;
