@@ -903,11 +903,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t v[32];
             tc::tmem_ld32(mine + L_::O + u, v);
             tc::tmem_wait_ld();
-            // a restart forgets the state whatever it held
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              v[i] = rd == 0.0f ? 0u
-                                : __float_as_uint(__uint_as_float(v[i]) * rd);
+            for (int i = 0; i < 32; i += 2) {
+              const float2 x =
+                  mul2(make_float2(__uint_as_float(v[i]),
+                                   __uint_as_float(v[i + 1])),
+                       make_float2(rd, rd));
+              v[i] = __float_as_uint(x.x);
+              v[i + 1] = __float_as_uint(x.y);
+            }
+            if (rd == 0.0f) {  // a restart forgets the state whatever it held
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0u;
+            }
             tc::tmem_st16(mine + L_::O + u, v);
             tc::tmem_st16(mine + L_::O + u + 16, v + 16);
           }
