@@ -23,7 +23,9 @@
  *   - Either decay may be NULL (0). A log decay of -infinity, or one below
  *     -87 (where its exponential is about to leave float32's normal numbers),
  *     starts the state anew at its token, whatever the state held. Others are finite numbers; positive
- *     ones are taken as they are.
+ *     ones are taken as they are, but where their sum over 128 tokens in a row
+ *     passes 88 (a growth beyond float32), results may be infinite or NaN even
+ *     if a token-by-token sum in float32 would not be.
  *   - lengths: NULL means every sequence has seqlen tokens. Else sequence b has
  *     lengths[b] of them (values outside 0..seqlen count as the nearer bound):
  *     what stands behind is not read into any result, whatever it holds; the

@@ -33,8 +33,8 @@
 // Bound by the tensor pipe's mma.sync rate and by what feeds it: six products
 // for float32 operands, at 40% of the pipe's cycles. 64 steps a chunk and 64
 // value columns a block leave room for two blocks an SM (one with three planes
-// of 128-wide keys). float32, 64 x up to 512 steps, 8 heads of 64: 194 us, the
-// bytes alone 42; backward, 3 x 1000 steps, 6 heads of 48 x 77: 188 us with
+// of 128-wide keys). float32, 64 x up to 512 steps, 8 heads of 64: 195 us, the
+// bytes alone 42; backward, 3 x 1000 steps, 6 heads of 48 x 77: 192 us with
 // its ten short launches.
 #pragma once
 
@@ -984,7 +984,7 @@ __global__ void __launch_bounds__(256)
   }
   // backwards, a whole segment at a time where it is one of 2048: thread i has
   // the i-th kRun tokens from the end, all on their way at once (8 x 24 heads
-  // of 2048 tokens: 18 us with a token a thread in eight rounds, 13.5 so)
+  // of 2048 tokens: 18 us with a token a thread in eight rounds, 13 so)
   constexpr int kRun = 8;
   double carry = end, part = 0.0;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;

@@ -39,7 +39,7 @@
 //
 // 148 heads x 8192 steps of (128, 128): 365 us, 3.4 TB/s (0.52 of the copy
 // rate); bound by a chunk's chain (state, its copy, products, weighted values,
-// update: 5.7 us), with 47% of the issue slots and 42% of the tensor pipe busy.
+// update: 5.7 us), with 45% of the issue slots and 43% of the tensor pipe busy.
 // With one plane, loops unrolled past the instruction cache took 370 us and
 // short ones 288; eight warps doing all of it in turn, 160 heads, 1.1 ms.
 #pragma once

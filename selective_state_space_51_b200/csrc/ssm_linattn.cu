@@ -97,10 +97,11 @@ size_t take(size_t *at, size_t floats) {
 // Segments: where one block for each sequence, head and tile leaves over half
 // of the GPU idle, a sequence is cut so that about two blocks (one of the
 // tensor-memory kernel) are there for each SM, of at least 128 (512) steps: 1 x
-// 65536 steps of 8 heads of 128 take 241 us in 18 segments a head; uncut,
-// eight SMs would go through 512 chunks of 4.5 us each. The states in front of
+// 65536 steps of 8 heads of 128 take 290 us in 18 segments a head; uncut,
+// eight SMs would go through 512 chunks of 5.7 us each. The states in front of
 // the segments cost one more reading of k and v, so a grid that fills the GPU
-// by itself is not cut.
+// by itself is not cut. (Two are counted for float32 with 128-wide keys too, of
+// which an SM holds one: its blocks then come in two rounds.)
 void cut(Plan *pl, int64_t blocks, int64_t L, int sms, Path path,
          int64_t most) {
   const int chunk = path == Path::kTc ? ssm::lat::kChunk : ssm::kLaChunk;
@@ -121,8 +122,9 @@ Plan plan_fwd(const ssm_linattn_dims &d, Path path, int sms) {
   const int64_t tiles = ceil_div(d.dv, ssm::kLaTile);
   const int64_t all = d.batch * d.heads;
   // One block an SM: where the last round of blocks would leave over half of
-  // the SMs idle, its heads are cut (4 x 8192 x 40 heads of 128: 550 us with
-  // 12 heads in a round of their own, 359 us with these cut).
+  // the SMs idle, its heads are cut (4 x 8192 x 40 heads of 128, one plane of
+  // the state: 550 us with 12 heads in a round of their own, 359 to 406 us with
+  // these cut).
   auto cut_for = [&](int64_t heads) {
     cut(&pl, heads * (path == Path::kTc ? 1 : tiles), d.seqlen, sms, path,
         int64_t(1) << 40);
@@ -586,7 +588,7 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
   const bool gate = dlog_decay || dhead_log_decay;
   // The heads' own gradient is float32 and sums differences over all steps:
   // the two planes that fit beside the stages there leave it 5.6e-5 off (8192
-  // steps of long memory), the other kernel's three planes 1e-6.
+  // steps of long memory), the other kernel's three planes 3e-7.
   const Path path = tc_takes(dims, dtype, q, k, v, {dy, dq, dk, dv}) &&
                             !dhead_log_decay
                         ? Path::kTc
