@@ -78,9 +78,15 @@ typedef struct {
 
 /*
  * ssm_linattn_workspace: bytes of device memory ssm_linattn_fwd (backward ==
- * 0) or ssm_linattn_bwd (backward != 0) needs for these dims on `device`; 0
- * where none is needed.
+ * 0) or ssm_linattn_bwd (backward == 1) needs for these dims on `device`,
+ * whatever its other arguments; 0 where none is needed. What a backward call
+ * does without may be added to the 1:
+ *   SSM_LINATTN_NO_HEAD_GRADIENT  : dhead_log_decay will be NULL;
+ *   SSM_LINATTN_NO_DECAY_GRADIENT : dlog_decay and dhead_log_decay will be.
  */
+#define SSM_LINATTN_NO_HEAD_GRADIENT 2
+#define SSM_LINATTN_NO_DECAY_GRADIENT 4
+
 SSM_API int ssm_linattn_workspace(int device, ssm_linattn_dims dims, int dtype,
                                   int backward, size_t *bytes);
 
@@ -122,7 +128,7 @@ SSM_API int ssm_linattn_step(int device, const void *q, const void *k,
  *   dhead_log_decay : [heads] float32, or NULL; each only with its input.
  *            Without either, dq and dk take fewer products.
  *   dh0    : [batch, heads, dk, dv] float32, or NULL.
- *   workspace : as above, for backward != 0.
+ *   workspace : as above, for the backward call.
  * The log decays' gradients at a token that starts the state anew are 0.
  * No output, and not the workspace, may overlap another or an input.
  */

@@ -488,8 +488,9 @@ __global__ void __launch_bounds__(kThreads, MINB)
     if constexpr (!STATE_ONLY) {
       // between tokens `edge` - 1 and `edge`: what the decay's gradient needs
       const int64_t edge = job.reverse ? rows.first + 1 : rows.first;
-      if (job.anchor && edge % kLaAnchor == 0 && edge > 0 && edge < len) {
-        const int64_t at = edge / kLaAnchor;
+      if (job.anchor && (edge & (p.anchor_len - 1)) == 0 && edge > 0 &&
+          edge < len) {
+        const int64_t at = edge / p.anchor_len;
         float *dst =
             job.anchor +
             ((bh * p.anchors + (job.reverse ? p.anchors - at : at)) *
@@ -927,8 +928,8 @@ __device__ __forceinline__ double block_sum(double v, double *red) {
 // of the state and its gradient is formed from the states the two passes left
 // there: what the differences are off by then adds up over one group only,
 // and the products' own errors over groups that know nothing of each other.
-// Where a float32 result comes of them, groups are kLaAnchor = 128 steps and
-// the sums 64-bit: of 2048 steps and in float32, the sum of a head's gradients
+// Where a float32 result comes of them, groups are 128 steps and the sums
+// 64-bit: of 2048 steps and in float32, the sum of a head's gradients
 // over 2 x 16384 steps was 2.7e-5 off (the plain form: 9e-7). Alone beside
 // bfloat16, segments of 2048 steps are as good as the output. A step that
 // starts the state anew has no gradient, and the sum starts from 0 there: the

@@ -9,9 +9,6 @@ namespace ssm {
 constexpr int kLaChunk = 64;   // steps per chunk of the chunked form
 constexpr int kLaTile = 64;    // value columns per block
 constexpr int kLaMaxKey = 128; // widest key (and, backward, value)
-// Steps from one state that the decay's gradient is anchored to to the next
-// (kernel_linattn.cuh), a multiple of the chunk.
-constexpr int kLaAnchor = 128;
 
 // One pass of linear attention with decay over every sequence and head:
 //   y_i = sp * sum_{j <= i} decay(j, i) (q_i . k_j) v_j + si * (...) of the
@@ -40,7 +37,7 @@ struct LaJob {
   double *seg_decay;                     // [bhs, nseg]
   float *anchor;                         // [b, heads, anchors, tiles, QD, 64]
                                          // or nullptr: the state in front of
-                                         // every kLaAnchor-th token
+                                         // every anchor_len-th token
 };
 
 struct LaParams {
@@ -52,13 +49,14 @@ struct LaParams {
   int heads;
   int nseg;                     // segments per sequence
   int64_t seg_len;              // steps per segment, a multiple of the chunk
-  int anchors;                  // groups of kLaAnchor tokens in a sequence
+  int anchors;                  // groups of anchor_len tokens in a sequence
+  int anchor_len;               // a power of 2, and of chunks
   int bh0, bhs;                 // the sequences' heads of this launch, counted
                                 // through all: bhs of them from bh0 on
 };
 
 // The log decay's gradient from the row dots and the states at the ends of
-// groups of steps (nseg of seg_len steps: kLaAnchor of them, or a segment).
+// groups of steps (nseg of seg_len steps: anchor_len of them, or a segment).
 struct LaGateParams {
   const float *rows_q, *rows_k;  // row dots of dq with q, of dk with k
   int parts;                           // of 32 columns each

@@ -27,11 +27,13 @@ constexpr int64_t kMaxSteps = int64_t(1) << 36;
 // The tensor-memory kernel counts tokens in 32 bits, up to two chunks past the
 // end.
 constexpr int64_t kMaxTcSteps = int64_t(1) << 30;
-// The decay's gradient sums differences inside a group of steps. The
-// tensor-memory kernel's passes, which run where that gradient is bfloat16
-// (rounded by 2^-9), leave states at the ends of segments only, and the segment
-// is the group; the other kernel's leave one every kLaAnchor steps.
+// The decay's gradient sums differences inside a group of steps: at most 2048
+// where it is bfloat16 (rounded by 2^-9), 128 where it is float32. The
+// tensor-memory kernel's passes, which are for the former only, leave states at
+// the ends of segments, and the segment is the group; the other kernel's leave
+// them wherever they are wanted.
 constexpr int64_t kGateSegment = 2048;
+constexpr int64_t kGateExact = 128;
 
 // Shared memory that lets one block of the tensor-memory kernel (which takes
 // all of TMEM) onto an SM at a time.
@@ -146,7 +148,9 @@ Plan plan_fwd(const ssm_linattn_dims &d, Path path, int sms) {
   return pl;
 }
 
-Plan plan_bwd(const ssm_linattn_dims &d, Path path, bool gate, int sms) {
+// gate: with the decays' gradients; exact: one of which is float32.
+Plan plan_bwd(const ssm_linattn_dims &d, Path path, bool gate, bool exact,
+              int sms) {
   Plan pl;
   const int64_t tk = ceil_div(d.dk, ssm::kLaTile),
                 tv = ceil_div(d.dv, ssm::kLaTile);
@@ -171,8 +175,8 @@ Plan plan_bwd(const ssm_linattn_dims &d, Path path, bool gate, int sms) {
     pl.groups = pl.nseg;
     pl.group_len = pl.seg_len;
     if (path == Path::kAny) {
-      pl.groups = int(ceil_div(d.seqlen, ssm::kLaAnchor));
-      pl.group_len = ssm::kLaAnchor;
+      pl.group_len = exact ? kGateExact : kGateSegment;
+      pl.groups = int(ceil_div(d.seqlen, pl.group_len));
       if (pl.groups > 1)
         for (size_t &a : pl.anchor)
           a = take(&pl.bytes, bh * pl.groups * tk * key_pad(d.dv) *
@@ -369,6 +373,7 @@ LaParams common(const ssm_linattn_dims &d, const Plan &pl,
   p.nseg = pl.nseg;
   p.seg_len = pl.seg_len;
   p.anchors = pl.groups;
+  p.anchor_len = int(pl.group_len);
   p.bhs = int(d.batch * d.heads);
   return p;
 }
@@ -399,12 +404,20 @@ int ssm_linattn_workspace(int device, ssm_linattn_dims dims, int dtype,
   if (rc != SSM_OK) return rc;
   for (Path path : {Path::kAny, Path::kTc}) {
     if (path == Path::kTc && (dtype != SSM_BF16 || dims.dv > 128)) continue;
-    if (backward) {
-      for (bool gate : {false, true})
-        *bytes = std::max(*bytes, plan_bwd(dims, path, gate, sms).bytes);
-    } else {
+    if (!backward) {
       *bytes = std::max(*bytes, plan_fwd(dims, path, sms).bytes);
+      continue;
     }
+    // every kind of call that is not ruled out
+    const bool gate = !(backward & SSM_LINATTN_NO_DECAY_GRADIENT),
+               head = gate && !(backward & SSM_LINATTN_NO_HEAD_GRADIENT) &&
+                      path == Path::kAny;
+    *bytes = std::max(*bytes, plan_bwd(dims, path, false, false, sms).bytes);
+    if (gate)
+      *bytes = std::max(*bytes, plan_bwd(dims, path, true, dtype == SSM_F32,
+                                         sms).bytes);
+    if (head)
+      *bytes = std::max(*bytes, plan_bwd(dims, path, true, true, sms).bytes);
   }
   return SSM_OK;
 }
@@ -593,7 +606,8 @@ int ssm_linattn_bwd(int device, const void *q, const void *k, const void *v,
                             !dhead_log_decay
                         ? Path::kTc
                         : Path::kAny;
-  const Plan pl = plan_bwd(dims, path, gate, sms);
+  const Plan pl =
+      plan_bwd(dims, path, gate, dtype == SSM_F32 || dhead_log_decay, sms);
   if (pl.bytes > workspace_bytes || (pl.bytes && !workspace))
     return SSM_ERR_INVALID;
   if (workspace && !aligned(workspace, 16)) return SSM_ERR_ALIGN;

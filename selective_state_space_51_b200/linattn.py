@@ -13,8 +13,13 @@ def _dims(dims):
     return ssm_linattn_dims(*[int(d) for d in dims])
 
 
+# of a backward call's workspace: what it does without
+NO_HEAD_GRADIENT, NO_DECAY_GRADIENT = 2, 4
+
+
 def ssm_linattn_workspace(device, dims, dtype, backward=False) -> int:
-    """Bytes of workspace a forward (or backward) call needs."""
+    """Bytes of workspace a forward (or backward) call needs; backward: True,
+    or 1 plus what the call does without."""
     n = ctypes.c_size_t(0)
     _check(library().ssm_linattn_workspace(int(device), _dims(dims),
                                            int(dtype), int(backward),
@@ -195,7 +200,7 @@ class LinearAttention:
         if h_last is None and want_last:
             h_last = torch.empty((dims[0], dims[2], dims[4], dims[5]),
                                  dtype=torch.float32, device=self.device)
-        ws, n = self._workspace(dims, code, False)
+        ws, n = self._workspace(dims, code, 0)
         _check(self._lib.ssm_linattn_fwd(
             self.device.index, q.data_ptr(), k.data_ptr(), v.data_ptr(),
             ptr(log_decay), ptr(head_log_decay), scale, ptr(lengths), ptr(h0),
@@ -266,7 +271,11 @@ class LinearAttention:
             dhead_log_decay=torch.empty((H,), **f)
             if head_log_decay is not None and decay_gradient else None,
             dh0=torch.empty((b, H, dk, dv), **f))
-        ws, n = self._workspace(dims, code, True)
+        kind = 1
+        if g["dhead_log_decay"] is None:
+            kind += (NO_DECAY_GRADIENT if g["dlog_decay"] is None
+                     else NO_HEAD_GRADIENT)
+        ws, n = self._workspace(dims, code, kind)
         _check(self._lib.ssm_linattn_bwd(
             self.device.index, q.data_ptr(), k.data_ptr(), v.data_ptr(),
             ptr(log_decay), ptr(head_log_decay), scale, ptr(lengths), ptr(h0),

@@ -136,3 +136,15 @@ def test_long_sums_of_padded_sequences(attn, path):
         assert np.all(tol <= 0.02 * dg)
         off = np.sqrt(((got[i, :n] - ref["dg"][i, :n]) ** 2).mean(0))
         assert np.all(off <= tol), (i, off / tol)
+
+
+@pytest.mark.parametrize("L", [2048, 2049, 4223])
+def test_long_sums_of_odd_bfloat16_rows(attn, L):
+    """Rows that the tensor-memory kernel does not take, the gradient bfloat16:
+    groups of 2048 steps, three planes."""
+    c = Case("bf16", 1, L, 2, 2, 33, 31, gate="token", rate=0.003)
+    ref = reference(c)
+    each, _ = D.tolerances(c, ref, 2048, D.DELTA["planes3"], "bf16")
+    assert np.all(each <= 0.02 * D.sizes(c, ref)[1])
+    off = D.rms(host(c.run_back(attn)["dlog_decay"]) - ref["dg"])
+    assert np.all(off <= each), off / each

@@ -81,3 +81,62 @@ def test_linear_attention(dtype):
             assert call(whole, n, {**args, k: part}) == S.SSM_ERR_INVALID, k
     torch.cuda.synchronize()
     assert S.ssm_linattn_sync_status(0) == S.SSM_OK
+
+
+NONE, TOKENS, HEADS = 1 + 4, 1 + 2, 1
+
+
+@pytest.mark.parametrize("dtype", [S.SSM_F32, S.SSM_BF16])
+@pytest.mark.parametrize("d", [64, 128, 45])
+@pytest.mark.parametrize("kind", [NONE, TOKENS, HEADS])
+def test_what_is_asked_for_is_enough_and_no_more(dtype, d, kind):
+    """A backward call runs in the workspace of its kind; the states that a
+    float32 gradient of the decay is anchored to, one for 128 steps, are in the
+    workspace of calls that have one only."""
+    ty = torch.float32 if dtype == S.SSM_F32 else torch.bfloat16
+    b, L, H = 1, 4096, 160
+    dims = (b, L, H, H, d, d, 0, 0, 0)
+    sizes = {k: S.ssm_linattn_workspace(0, dims, dtype, k)
+             for k in (NONE, TOKENS, HEADS)}
+    assert sizes[NONE] <= sizes[TOKENS] <= sizes[HEADS]
+    assert S.ssm_linattn_workspace(0, dims, dtype, True) == sizes[HEADS]
+    pad = 64 if d <= 64 else 128
+    anchors = 2 * H * (L // 128) * pad * pad * 4
+    # (and as many segments' states as there may be: three of each)
+    segments = 3 * H * (L // 2048) * pad * pad * 4
+    rows = 2 * H * L * 2 * (pad // 64) * 4
+    exact = kind == HEADS or (dtype == S.SSM_F32 and kind == TOKENS)
+    assert (sizes[kind] >= anchors) == exact
+    assert sizes[kind] <= exact * anchors + 2 * segments + rows + (1 << 24)
+    z = lambda *s, t=ty: torch.zeros(*s, dtype=t, device="cuda")  # noqa: E731
+    q = z(b, L, H, d)
+    out = [torch.empty_like(q) for _ in range(3)]
+    log, head = z(b, L, H), z(H, t=torch.float32)
+    n = sizes[kind]
+    rc = S.ssm_linattn_bwd(
+        0, q, q, q, log, head, 1.0, None, None, q, None, *out,
+        None if kind == NONE else torch.empty_like(log),
+        torch.empty_like(head) if kind == HEADS else None, None,
+        z(max(n, 1), t=torch.uint8) if n else None, n, dims, dtype,
+        check=False)
+    torch.cuda.synchronize()
+    assert rc == S.SSM_OK
+
+
+def test_the_class_asks_for_what_it_needs():
+    """128-wide bfloat16 heads with the tokens' decay gradient: no anchors."""
+    attn = S.LinearAttention(0)
+    b, L, H, d = 1, 4096, 160, 128
+    q = torch.zeros(b, L, H, d, dtype=torch.bfloat16, device="cuda")
+    log = q[..., 0].contiguous()
+    attn.backward(q, q, q, q, log_decay=log)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    g = attn.backward(q, q, q, q, log_decay=log)
+    torch.cuda.synchronize()
+    kept = torch.cuda.memory_allocated() - before
+    used = torch.cuda.max_memory_allocated() - before
+    anchors = 2 * H * (L // 128) * d * d * 4
+    assert used - kept < anchors / 2
+    del g
