@@ -468,6 +468,7 @@ class SelectiveScan:
 
 from .layernorm import (LayerNorm, ssm_layernorm_bwd,  # noqa: E402,F401
                         ssm_layernorm_fwd, ssm_layernorm_workspace)
-from .linattn import (LinearAttention, ssm_linattn_bwd,  # noqa: E402,F401
-                      ssm_linattn_fwd, ssm_linattn_step,
+from .linattn import (SSM_LINATTN_NO_DECAY_GRADIENT,  # noqa: E402,F401
+                      SSM_LINATTN_NO_HEAD_GRADIENT, LinearAttention,
+                      ssm_linattn_bwd, ssm_linattn_fwd, ssm_linattn_step,
                       ssm_linattn_sync_status, ssm_linattn_workspace)

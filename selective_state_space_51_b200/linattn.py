@@ -14,7 +14,7 @@ def _dims(dims):
 
 
 # of a backward call's workspace: what it does without
-NO_HEAD_GRADIENT, NO_DECAY_GRADIENT = 2, 4
+SSM_LINATTN_NO_HEAD_GRADIENT, SSM_LINATTN_NO_DECAY_GRADIENT = 2, 4
 
 
 def ssm_linattn_workspace(device, dims, dtype, backward=False) -> int:
@@ -273,8 +273,8 @@ class LinearAttention:
             dh0=torch.empty((b, H, dk, dv), **f))
         kind = 1
         if g["dhead_log_decay"] is None:
-            kind += (NO_DECAY_GRADIENT if g["dlog_decay"] is None
-                     else NO_HEAD_GRADIENT)
+            kind += (SSM_LINATTN_NO_DECAY_GRADIENT if g["dlog_decay"] is None
+                     else SSM_LINATTN_NO_HEAD_GRADIENT)
         ws, n = self._workspace(dims, code, kind)
         _check(self._lib.ssm_linattn_bwd(
             self.device.index, q.data_ptr(), k.data_ptr(), v.data_ptr(),

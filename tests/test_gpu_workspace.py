@@ -83,7 +83,8 @@ def test_linear_attention(dtype):
     assert S.ssm_linattn_sync_status(0) == S.SSM_OK
 
 
-NONE, TOKENS, HEADS = 1 + 4, 1 + 2, 1
+NONE = 1 + S.SSM_LINATTN_NO_DECAY_GRADIENT
+TOKENS, HEADS = 1 + S.SSM_LINATTN_NO_HEAD_GRADIENT, 1
 
 
 @pytest.mark.parametrize("dtype", [S.SSM_F32, S.SSM_BF16])
